@@ -79,10 +79,13 @@ typedef int32_t csa_status;
 /* ---- formats ------------------------------------------------------------ */
 #define CSA_KV_F32 0
 #define CSA_KV_FP8_BF16 1
+#define CSA_KV_ACT 2 /* gqa_*: rows in the activation type                 */
+#define CSA_KV_FP8 3 /* gqa_*: E4M3 rows, one fp32 scale each              */
 #define CSA_IDX_F32 0
 #define CSA_IDX_MXFP4 1
 #define CSA_ACT_F32 0
 #define CSA_ACT_BF16 1
+#define CSA_ACT_F16 2 /* gqa_* only                                        */
 #define CSA_SCORE_F32 0  /* index scores kept in fp32 before selection      */
 #define CSA_SCORE_BF16 1 /* index scores rounded to BF16 (RNE) before it   */
 
@@ -384,6 +387,130 @@ csa_status csa_state_append(const csa_params* params, const void* kv_new, const 
  * that sequence's rings untouched. */
 csa_status csa_state_restore(const csa_params* params, const int32_t* pos, const csa_ckpt* ckpt,
                              csa_state state, int32_t* err, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Grouped-query attention over a paged cache: gqa_cache_append,
+ * gqa_decode_attn, gqa_prompt_attn.  (No counterpart in the DeepSeek-V4
+ * write-ups, which use it only as the baseline their cache sizes are quoted
+ * against: BF16 keys and values, 8 KV heads.)  For layers whose keys and
+ * values are kept raw, one pair of rows per token and KV head, beside the
+ * compressed layers above; sinks and sliding windows are those of
+ * csa_sparse_attn.
+ *
+ *   B           sequences (1..2048)
+ *   n_heads     query heads (1..128), a multiple of n_kv_heads; query head h
+ *               reads KV head h / (n_heads / n_kv_heads)
+ *   d           head dim, 64 or 128
+ *   r           rotated dims: the last r of d (0 <= r <= d, a multiple of
+ *               8); read by gqa_cache_append only
+ *   page        tokens per cache page: 16, 32, 64, 128 or 256 (ignored by
+ *               gqa_prompt_attn)
+ *   window      a query at position t sees the keys at t-window+1 .. t;
+ *               0: every key up to t
+ *   kv_fmt      CSA_KV_ACT or CSA_KV_FP8 (ignored by gqa_prompt_attn)
+ *   act_fmt     CSA_ACT_BF16 or CSA_ACT_F16: queries, new keys and values,
+ *               outputs
+ *   softmax_scale   logit = softmax_scale * q.k
+ *   rope_theta  pair j of the last r dims (dims d-r+2j, d-r+2j+1) turns by
+ *               pos * theta^(-2j/r)
+ */
+typedef struct gqa_params {
+  int32_t B, n_heads, n_kv_heads, d, r, page, window;
+  int32_t kv_fmt, act_fmt;
+  float softmax_scale, rope_theta;
+} gqa_params;
+
+/* Rows of heads in act_fmt: head h of row i is the d contiguous elements at
+ * ptr + i * row_stride + h * head_stride (strides in elements, multiples
+ * of 8 and at least d; ptr 16-byte aligned).  Slices of a fused projection and
+ * head-major tensors are passed as they are.  Rows that are written must not
+ * overlap. */
+typedef struct gqa_rows {
+  void* ptr;
+  int64_t row_stride, head_stride;
+} gqa_rows;
+
+/* The paged cache.  Position p of sequence b is slot p % page of page
+ * table[b][p / page] (int32 [B][table_cols]).
+ *   k, v              [n_pages][n_kv_heads][page][d]: act_fmt (CSA_KV_ACT),
+ *                     or E4M3 codes (CSA_KV_FP8, value = code * scale)
+ *   k_scale, v_scale  [n_pages][n_kv_heads][page] fp32 (CSA_KV_FP8, else NULL)
+ * Table entries and page slots that no sequence reaches are never read. */
+typedef struct gqa_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t n_pages;
+} gqa_cache;
+
+/* gqa_cache_append: the tokens cu[b] .. cu[b+1]-1 of the packed rows are
+ * sequence b's next tokens, at positions pos0[b], pos0[b]+1, ...  Their keys
+ * are turned by their positions and stored with their values in the cache;
+ * the turned queries and keys are also written to q_out and k_out.
+ *   q, q_out    [n_tokens][n_heads]; both ptr NULL to leave queries alone;
+ *               q_out may be q itself
+ *   k, v        [n_tokens][n_kv_heads]
+ *   k_out       [n_tokens][n_kv_heads]; ptr NULL: not written; may be k
+ *   cu          int32 [B+1], not decreasing, cu[0] = 0, cu[B] <= n_tokens;
+ *               rows from cu[B] on are neither read nor written
+ *   pos0        int32 [B]
+ * The turn is computed in fp32 (angles reduced in fp64).  CSA_KV_ACT rounds
+ * the result once; CSA_KV_FP8 stores scale = amax/448 over the row's d values
+ * (1 for a row of zeros) and the E4M3 codes of value / scale, both from the
+ * fp32 result.  A token whose position is negative or past the table raises
+ * CSA_DEV_ERR_RANGE, one whose page is not in [0, n_pages) CSA_DEV_ERR_INDEX;
+ * it is not stored (q_out and k_out are written all the same).  Two tokens
+ * of one call must not share a cache slot. */
+csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
+                            gqa_rows v, int64_t n_tokens, const int32_t* cu,
+                            const int32_t* pos0, gqa_cache cache,
+                            const int32_t* table, int64_t table_cols,
+                            gqa_rows q_out, gqa_rows k_out, int32_t* err,
+                            void* stream);
+
+/* gqa_decode_attn: the last T tokens of every sequence attend to the cache.
+ * Query row b*T + tau sits at position t = lens[b] - T + tau and sees the
+ * keys at max(0, t-window+1) .. t:
+ *   z_j = softmax_scale * q.k_j,  p_j = exp(z_j) / (exp(sink[h]) + sum exp(z_j))
+ *   o   = sum_j p_j v_j, written in act_fmt; zeros where no key is seen
+ *   q, out      [B*T][n_heads]
+ *   lens        int32 [B]: keys in the cache, the new tokens included
+ *   n_max       host upper bound on lens (n_max <= table_cols * page);
+ *               a longer sequence is read up to n_max with CSA_DEV_ERR_RANGE
+ *   sink        fp32 [n_heads], or NULL for none
+ *   ws          workspace of gqa_decode_attn_workspace_bytes(params, T, n_max)
+ * T is at most 64.  The keys of a page not in [0, n_pages) are skipped with
+ * CSA_DEV_ERR_INDEX.  What masked slots hold (infinities and NaN included)
+ * does not matter; logits of seen keys must be finite in fp32.  How a
+ * sequence's keys are split depends on its own length, T and the window
+ * alone, and partial results are joined in a fixed order: a query's output
+ * is bit-identical run to run and whatever batch it is in. */
+csa_status gqa_decode_attn(const gqa_params* params, gqa_rows q, gqa_cache cache,
+                           const int32_t* table, int64_t table_cols,
+                           const int32_t* lens, int32_t T, int32_t n_max,
+                           const float* sink, gqa_rows out, void* ws,
+                           size_t ws_bytes, int32_t* err, void* stream);
+size_t gqa_decode_attn_workspace_bytes(const gqa_params* params, int32_t T,
+                                       int32_t n_max);
+
+/* gqa_prompt_attn: causal attention over packed prompts.  Sequence b's
+ * queries are rows cu_q[b] .. cu_q[b+1]-1 of q and its keys and values rows
+ * cu_k[b] .. cu_k[b+1]-1 of k and v; the last query sits at the last key, so
+ * query i of n sits at t = (keys - n) + i and sees the keys at
+ * max(0, t-window+1) .. t (none where t < 0: its output is zeros).
+ * Softmax, sink and output as in gqa_decode_attn.
+ *   q, out      [n_q][n_heads]
+ *   k, v        [n_k][n_kv_heads]
+ *   cu_q, cu_k  int32 [B+1], not decreasing, first 0, last <= n_q / n_k; output
+ *               rows from cu_q[B] on are left as they are
+ * A sequence whose rows are not inside n_q / n_k is left out with
+ * CSA_DEV_ERR_RANGE. */
+csa_status gqa_prompt_attn(const gqa_params* params, gqa_rows q, gqa_rows k,
+                           gqa_rows v, int64_t n_q, int64_t n_k,
+                           const int32_t* cu_q, const int32_t* cu_k,
+                           const float* sink, gqa_rows out, int32_t* err,
+                           void* stream);
 
 /* Human-readable name of a csa_status. */
 const char* csa_status_string(csa_status s);

@@ -23,15 +23,17 @@ __all__ = [
     "hca_dense_attn_workspace_bytes", "csa_index_topk_noalloc", "csa_index_compress", "csa_index_quantize",
     "CsaState", "CsaCkpt", "csa_state_append", "csa_state_restore", "KV_F32", "KV_FP8_BF16", "IDX_F32", "IDX_MXFP4",
     "ACT_F32", "ACT_BF16", "SCORE_F32", "SCORE_BF16", "DEV_ERR_INDEX", "DEV_ERR_RANGE",
+    "GqaParams", "GqaRows", "GqaCache", "make_gqa_params", "make_gqa_cache", "gqa_cache_append", "gqa_decode_attn",
+    "gqa_decode_attn_workspace_bytes", "gqa_prompt_attn", "KV_ACT", "KV_FP8", "ACT_F16",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libcsa.so")
 
-KV_F32, KV_FP8_BF16 = 0, 1
+KV_F32, KV_FP8_BF16, KV_ACT, KV_FP8 = 0, 1, 2, 3
 SCORE_F32, SCORE_BF16 = 0, 1
 IDX_F32, IDX_MXFP4 = 0, 1
-ACT_F32, ACT_BF16 = 0, 1
+ACT_F32, ACT_BF16, ACT_F16 = 0, 1, 2
 DEV_ERR_INDEX, DEV_ERR_RANGE = 1, 2
 
 STATUS = {0: "CSA_OK", -1: "CSA_ERR_INVALID", -2: "CSA_ERR_UNSUPPORTED", -3: "CSA_ERR_ALIGN",
@@ -41,7 +43,8 @@ EXPORTS = ["csa_compress", "hca_compress", "csa_index_topk", "csa_index_topk_wor
            "csa_sparse_attn", "csa_sparse_attn_workspace_bytes", "hca_dense_attn",
            "hca_dense_attn_workspace_bytes", "csa_status_string", "csa_last_error_string",
            "csa_index_topk_noalloc", "csa_index_compress", "csa_index_quantize", "csa_state_append",
-           "csa_state_restore"]
+           "csa_state_restore", "gqa_cache_append", "gqa_decode_attn", "gqa_decode_attn_workspace_bytes",
+           "gqa_prompt_attn"]
 
 
 class CsaError(RuntimeError):
@@ -71,6 +74,21 @@ class CsaCkpt(ctypes.Structure):
     _fields_ = [("win_rows", ctypes.c_void_p), ("win_scale", ctypes.c_void_p), ("a", ctypes.c_void_p),
                 ("b", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("n_slots", ctypes.c_int32),
                 ("every", ctypes.c_int32)]
+
+
+class GqaParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "n_heads", "n_kv_heads", "d", "r", "page", "window", "kv_fmt", "act_fmt")] + \
+               [(n, ctypes.c_float) for n in ("softmax_scale", "rope_theta")]
+
+
+class GqaRows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class GqaCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64)]
 
 
 _lib = None
@@ -114,6 +132,16 @@ def lib(path: str | None = None):
     L.csa_state_append.restype = _I32
     L.csa_state_restore.argtypes = [_P, _V, ctypes.POINTER(CsaCkpt), CsaState, _V, _V]
     L.csa_state_restore.restype = _I32
+    G = ctypes.POINTER(GqaParams)
+    R = GqaRows
+    L.gqa_cache_append.argtypes = [G, R, R, R, _I64, _V, _V, GqaCache, _V, _I64, R, R, _V, _V]
+    L.gqa_cache_append.restype = _I32
+    L.gqa_decode_attn.argtypes = [G, R, GqaCache, _V, _I64, _V, _I32, _I32, _V, R, _V, _SZ, _V, _V]
+    L.gqa_decode_attn.restype = _I32
+    L.gqa_decode_attn_workspace_bytes.argtypes = [G, _I32, _I32]
+    L.gqa_decode_attn_workspace_bytes.restype = _SZ
+    L.gqa_prompt_attn.argtypes = [G, R, R, R, _I64, _I64, _V, _V, _V, R, _V, _V]
+    L.gqa_prompt_attn.restype = _I32
     L.csa_status_string.argtypes = [_I32]
     L.csa_status_string.restype = ctypes.c_char_p
     L.csa_last_error_string.argtypes = []
@@ -282,3 +310,90 @@ def hca_dense_attn(params, q, cache_rows, cache_scale, win_rows, win_scale, sink
                               _ptr(out), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
                               _ptr(err), _stream(stream))
     _check("hca_dense_attn", st)
+
+
+def make_gqa_params(*, B, n_heads, n_kv_heads, d, r=0, page=64, window=0, kv_fmt=KV_ACT, act_fmt=ACT_BF16,
+                    softmax_scale=1.0, rope_theta=1e4) -> GqaParams:
+    return GqaParams(B, n_heads, n_kv_heads, d, r, page, window, kv_fmt, act_fmt, softmax_scale, rope_theta)
+
+
+def make_gqa_cache(k, v, k_scale=None, v_scale=None) -> GqaCache:
+    """gqa_cache over device tensors: k and v [n_pages, n_kv_heads, page, d]
+    (+ scales [n_pages, n_kv_heads, page] for an FP8 cache).  The tensors
+    stay the caller's: keep them alive as long as the handle is used."""
+    if k.shape != v.shape or (k_scale is None) != (v_scale is None):
+        raise ValueError("keys and values are cached alike")
+    return GqaCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0])
+
+
+_NO_ROWS = GqaRows(None, 0, 0)
+_ACT_DTYPES = {ACT_BF16: "torch.bfloat16", ACT_F16: "torch.float16"}
+
+
+def _rows(x, params, heads):
+    """gqa_rows of a CUDA tensor [n, heads, d] of the activation type; only
+    its last dim has to be contiguous."""
+    if not x.is_cuda:
+        raise TypeError("libcsa takes CUDA tensors (device pointers); got a host array")
+    if str(x.dtype) != _ACT_DTYPES.get(params.act_fmt, str(x.dtype)):
+        raise TypeError(f"act_fmt says {_ACT_DTYPES[params.act_fmt]}, got {x.dtype}")
+    n, h, d = x.shape
+    if h != heads or d != params.d:
+        raise ValueError(f"expected [n, {heads}, {params.d}], got {tuple(x.shape)}")
+    sn, sh, sd = x.stride()
+    if sd != 1:
+        raise ValueError("the last dim of a row tensor has to be contiguous")
+    if n < 2:
+        sn = max(sn, d)  # the stride of a single row is never used
+    if h < 2:
+        sh = max(sh, d)
+    return GqaRows(x.data_ptr(), sn, sh)
+
+
+def gqa_cache_append(params, q, k, v, cu, pos0, cache, table, q_out=None, k_out=None, err=None, stream=None):
+    """Store the packed tokens ``k``/``v`` ([n, n_kv_heads, d]; sequence b's
+    are rows cu[b]..cu[b+1]-1, from position pos0[b] on) in the paged
+    ``cache`` through ``table`` ([B, cols]), keys turned by their positions.
+    Turned queries (``q`` [n, n_heads, d], or None) go to ``q_out``, turned
+    keys to ``k_out`` (both may be the inputs)."""
+    hk = params.n_kv_heads
+    if v.shape[0] != k.shape[0] or any(x is not None and x.shape[0] != k.shape[0] for x in (q, q_out, k_out)):
+        raise ValueError("q, k, v, q_out and k_out have the same rows")
+    st = lib().gqa_cache_append(
+        ctypes.byref(params), _NO_ROWS if q is None else _rows(q, params, params.n_heads), _rows(k, params, hk),
+        _rows(v, params, hk), k.shape[0], _ptr(cu), _ptr(pos0), cache, _ptr(table), table.shape[1],
+        _NO_ROWS if q_out is None else _rows(q_out, params, params.n_heads),
+        _NO_ROWS if k_out is None else _rows(k_out, params, hk), _ptr(err), _stream(stream))
+    _check("gqa_cache_append", st)
+
+
+def gqa_decode_attn_workspace_bytes(params, T, n_max):
+    return int(lib().gqa_decode_attn_workspace_bytes(ctypes.byref(params), int(T), int(n_max)))
+
+
+def gqa_decode_attn(params, q, cache, table, lens, T, n_max, out, ws=None, sink=None, err=None, stream=None):
+    """The last T tokens of every sequence (``q``, ``out`` [B*T, n_heads, d])
+    attend to the lens[b] <= n_max cached keys of their sequence; ``ws`` is a
+    CUDA byte tensor of gqa_decode_attn_workspace_bytes(params, T, n_max)."""
+    if q.shape[0] != params.B * T or out.shape[0] != params.B * T:
+        raise ValueError("q and out have B * T rows")
+    st = lib().gqa_decode_attn(
+        ctypes.byref(params), _rows(q, params, params.n_heads), cache, _ptr(table), table.shape[1], _ptr(lens), T,
+        n_max, _ptr(sink), _rows(out, params, params.n_heads), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _ptr(err), _stream(stream))
+    _check("gqa_decode_attn", st)
+
+
+def gqa_prompt_attn(params, q, k, v, cu_q, cu_k, out, sink=None, err=None, stream=None):
+    """Causal attention over packed prompts: sequence b's queries are rows
+    cu_q[b]..cu_q[b+1]-1 of ``q`` and ``out`` ([n_q, n_heads, d]), its keys
+    and values rows cu_k[b]..cu_k[b+1]-1 of ``k`` and ``v`` ([n_k,
+    n_kv_heads, d]); the last query sits at the last key."""
+    if out.shape[0] != q.shape[0] or v.shape[0] != k.shape[0]:
+        raise ValueError("q and out have the same rows, and k and v")
+    hk = params.n_kv_heads
+    st = lib().gqa_prompt_attn(
+        ctypes.byref(params), _rows(q, params, params.n_heads), _rows(k, params, hk), _rows(v, params, hk),
+        q.shape[0], k.shape[0], _ptr(cu_q), _ptr(cu_k), _ptr(sink), _rows(out, params, params.n_heads), _ptr(err),
+        _stream(stream))
+    _check("gqa_prompt_attn", st)

@@ -302,6 +302,97 @@ csa_status csa_state_restore(const csa_params* p, const int32_t* pos, const csa_
   return launched(csa::launch_state_restore(*p, pos, *ckpt, state, err, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static csa_status check_gqa(const gqa_params* p) {
+  if (!p) return CSA_ERR_INVALID;
+  if (p->B < 1 || p->n_heads < 1 || p->n_kv_heads < 1 || p->window < 0) return CSA_ERR_INVALID;
+  if (p->n_heads % p->n_kv_heads) return CSA_ERR_INVALID;
+  if (p->B > 2048 || p->n_heads > 128) return CSA_ERR_UNSUPPORTED;
+  if (p->d != 64 && p->d != 128) return CSA_ERR_UNSUPPORTED;
+  if (p->act_fmt != CSA_ACT_BF16 && p->act_fmt != CSA_ACT_F16) return CSA_ERR_UNSUPPORTED;
+  if (!(p->softmax_scale > 0.f && p->softmax_scale <= 3.0e38f)) return CSA_ERR_INVALID;
+  return CSA_OK;
+}
+
+static csa_status check_rows(const gqa_params* p, const gqa_rows& x) {
+  constexpr int64_t kMost = (int64_t)1 << 38;  // TMA strides end at 2^40 bytes
+  if (!x.ptr || x.row_stride < p->d || x.head_stride < p->d) return CSA_ERR_INVALID;
+  if (x.row_stride > kMost || x.head_stride > kMost) return CSA_ERR_UNSUPPORTED;
+  if (!aligned16(x.ptr) || (x.row_stride & 7) || (x.head_stride & 7)) return CSA_ERR_ALIGN;
+  return CSA_OK;
+}
+
+static csa_status check_gqa_cache(const gqa_params* p, const gqa_cache& c, const int32_t* table, int64_t table_cols) {
+  if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128 && p->page != 256) return CSA_ERR_UNSUPPORTED;
+  if (p->kv_fmt != CSA_KV_ACT && p->kv_fmt != CSA_KV_FP8) return CSA_ERR_UNSUPPORTED;
+  if (!c.k || !c.v || !table || c.n_pages < 1 || table_cols < 1) return CSA_ERR_INVALID;
+  // page ids and positions are 32-bit
+  if (c.n_pages > INT32_MAX / p->n_kv_heads || table_cols > INT32_MAX / p->page) return CSA_ERR_UNSUPPORTED;
+  for (const void* ptr : {(const void*)c.k, (const void*)c.v, (const void*)table})
+    if (!aligned16(ptr)) return CSA_ERR_ALIGN;
+  if (p->kv_fmt == CSA_KV_FP8) {
+    if (!c.k_scale || !c.v_scale) return CSA_ERR_INVALID;
+    if (!aligned16(c.k_scale) || !aligned16(c.v_scale)) return CSA_ERR_ALIGN;
+  }
+  return CSA_OK;
+}
+
+csa_status gqa_cache_append(const gqa_params* p, gqa_rows q, gqa_rows k, gqa_rows v, int64_t n_tokens,
+                            const int32_t* cu, const int32_t* pos0, gqa_cache cache, const int32_t* table,
+                            int64_t table_cols, gqa_rows q_out, gqa_rows k_out, int32_t* err, void* stream) {
+  csa_status s = check_gqa(p);
+  if (s != CSA_OK) return s;
+  if (p->r < 0 || p->r > p->d || (p->r & 7)) return CSA_ERR_UNSUPPORTED;
+  if (!(p->rope_theta > 0.f)) return CSA_ERR_INVALID;
+  if (!cu || !pos0 || n_tokens < 0 || !q.ptr != !q_out.ptr) return CSA_ERR_INVALID;
+  if (n_tokens > INT32_MAX) return CSA_ERR_UNSUPPORTED;
+  if (!aligned16(cu) || !aligned16(pos0)) return CSA_ERR_ALIGN;
+  if ((s = check_gqa_cache(p, cache, table, table_cols)) != CSA_OK) return s;
+  if (q.ptr && ((s = check_rows(p, q)) != CSA_OK || (s = check_rows(p, q_out)) != CSA_OK)) return s;
+  if ((s = check_rows(p, k)) != CSA_OK || (s = check_rows(p, v)) != CSA_OK) return s;
+  if (k_out.ptr && (s = check_rows(p, k_out)) != CSA_OK) return s;
+  if (n_tokens == 0) return CSA_OK;
+  return launched(csa::launch_gqa_append(*p, q, k, v, n_tokens, cu, pos0, cache, table, table_cols, q_out, k_out, err,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t gqa_decode_attn_workspace_bytes(const gqa_params* p, int32_t T, int32_t n_max) {
+  if (check_gqa(p) != CSA_OK || T < 1 || T > 64 || n_max < 0) return 0;
+  return csa::gqa_decode_workspace_bytes(*p, T, n_max);
+}
+
+csa_status gqa_decode_attn(const gqa_params* p, gqa_rows q, gqa_cache cache, const int32_t* table, int64_t table_cols,
+                           const int32_t* lens, int32_t T, int32_t n_max, const float* sink, gqa_rows out, void* ws,
+                           size_t ws_bytes, int32_t* err, void* stream) {
+  csa_status s = check_gqa(p);
+  if (s != CSA_OK) return s;
+  if (!lens || T < 1 || n_max < 0) return CSA_ERR_INVALID;
+  if (T > 64) return CSA_ERR_UNSUPPORTED;
+  if ((s = check_gqa_cache(p, cache, table, table_cols)) != CSA_OK) return s;
+  if (n_max > table_cols * p->page) return CSA_ERR_INVALID;
+  if ((s = check_rows(p, q)) != CSA_OK || (s = check_rows(p, out)) != CSA_OK) return s;
+  if (!aligned16(lens) || (sink && !aligned16(sink))) return CSA_ERR_ALIGN;
+  const size_t need = csa::gqa_decode_workspace_bytes(*p, T, n_max);
+  if (ws_bytes < need || (need && !ws)) return CSA_ERR_WORKSPACE;
+  if (ws && !aligned16(ws)) return CSA_ERR_ALIGN;
+  return launched(csa::launch_gqa_decode(*p, q, cache, table, table_cols, lens, T, n_max, sink, out, ws, err,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+csa_status gqa_prompt_attn(const gqa_params* p, gqa_rows q, gqa_rows k, gqa_rows v, int64_t n_q, int64_t n_k,
+                           const int32_t* cu_q, const int32_t* cu_k, const float* sink, gqa_rows out, int32_t* err,
+                           void* stream) {
+  csa_status s = check_gqa(p);
+  if (s != CSA_OK) return s;
+  if (!cu_q || !cu_k || n_q < 0 || n_k < 0) return CSA_ERR_INVALID;
+  if (n_q > INT32_MAX / 2 || n_k > INT32_MAX / 2) return CSA_ERR_UNSUPPORTED;
+  if (!aligned16(cu_q) || !aligned16(cu_k) || (sink && !aligned16(sink))) return CSA_ERR_ALIGN;
+  if (n_q == 0) return CSA_OK;
+  if ((s = check_rows(p, q)) != CSA_OK || (s = check_rows(p, out)) != CSA_OK) return s;
+  if (n_k > 0 && ((s = check_rows(p, k)) != CSA_OK || (s = check_rows(p, v)) != CSA_OK)) return s;
+  return launched(csa::launch_gqa_prompt(*p, q, k, v, n_q, n_k, cu_q, cu_k, sink, out, err,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
 const char* csa_last_error_string(void) { return g_last_error; }
 
 const char* csa_status_string(csa_status s) {

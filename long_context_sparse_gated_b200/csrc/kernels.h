@@ -110,4 +110,18 @@ cudaError_t launch_attn(const csa_params& p, const void* q, const csa_kv& cache,
                         int n_sel, bool dense, void* out, float* ws, int32_t* err,
                         cudaStream_t st);
 
+cudaError_t launch_gqa_append(const gqa_params& p, const gqa_rows& q, const gqa_rows& k, const gqa_rows& v,
+                              int64_t n_tokens, const int32_t* cu, const int32_t* pos0, const gqa_cache& cache,
+                              const int32_t* table, int64_t table_cols, const gqa_rows& q_out, const gqa_rows& k_out,
+                              int32_t* err, cudaStream_t st);
+
+size_t gqa_decode_workspace_bytes(const gqa_params& p, int T, int n_max);
+cudaError_t launch_gqa_decode(const gqa_params& p, const gqa_rows& q, const gqa_cache& cache, const int32_t* table,
+                              int64_t table_cols, const int32_t* lens, int T, int n_max, const float* sink,
+                              const gqa_rows& out, void* ws, int32_t* err, cudaStream_t st);
+
+cudaError_t launch_gqa_prompt(const gqa_params& p, const gqa_rows& q, const gqa_rows& k, const gqa_rows& v,
+                              int64_t n_q, int64_t n_k, const int32_t* cu_q, const int32_t* cu_k, const float* sink,
+                              const gqa_rows& out, int32_t* err, cudaStream_t st);
+
 }  // namespace csa
