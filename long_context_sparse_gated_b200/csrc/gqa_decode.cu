@@ -62,6 +62,7 @@ using namespace gqa;
 constexpr int kTile = 64;         // keys per stage
 constexpr int kConsumers = 8;     // warps
 constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kObufPitch = 68;    // floats per row of the join buffer (a warp's stores hit 32 banks)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLogScale = -90.f, kMaxLogScale = 90.f;
 
@@ -170,8 +171,13 @@ struct Layout {
   static constexpr int kOperand = kTile * kRowBytes;           // K or V of a tile
   static constexpr int kScales = kFp8 ? kTile * 4 : 0;         // K or V scales of a tile
   static constexpr int kStage = 2 * kOperand;
-  static constexpr int kObuf = kConsumers * 8 * (kD + 4) * 4;  // eight warps' outputs of 8 rows
-  static constexpr int kStages = kStage >= 32768 ? 5 : (kStage >= 16384 ? 9 : 16);
+  static constexpr int kObuf = kConsumers * 8 * kObufPitch * 4;  // eight warps' outputs: 8 rows, 64 dims
+  // even, so that a stage always belongs to the same group of warps: a group
+  // then waits for every phase of its stages' barriers in turn (with an odd
+  // count it would meet every second phase, which a parity cannot tell from
+  // the one before it)
+  static constexpr int kStages = kStage >= 32768 ? 6 : (kFp8 ? (kD == 128 ? 10 : 20) : 12);
+  static_assert(kStages % 2 == 0, "a stage belongs to one group");
   static constexpr size_t kSmem = 1024 + (size_t)kStages * (kStage + 2 * kScales) + kObuf;
 };
 
@@ -604,26 +610,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, red_m[par][w][8 * nt + 2 * q4 + e]);
           f[e] = M == -INFINITY ? 0.f : ex2(m[nt][e] - M);
         }
-        constexpr int kLd = kD + 4;  // row pitch: a warp's stores hit 32 banks
-        if (nt > 0) sm100::named_bar_sync(1, 32 * kConsumers);  // the last rows' sums are read
 #pragma unroll
-        for (int mt = 0; mt < kD / 16; ++mt)
+        for (int hh = 0; hh < kD / 64; ++hh) {  // 64 dims (four m-tiles) at a time
+          if (nt + hh > 0) sm100::named_bar_sync(1, 32 * kConsumers);  // the last ones' sums are read
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int dim = kFp8 ? kD / 8 * g + 2 * mt + (e >> 1) : 16 * mt + g + 8 * (e >> 1);
-            obuf[(warp * 8 + 2 * q4 + (e & 1)) * kLd + dim] = f[e & 1] == 0.f ? 0.f : o[mt][nt][e] * f[e & 1];
-          }
-        sm100::named_bar_sync(1, 32 * kConsumers);
-        for (int at = threadIdx.x * 4; at < 8 * kD; at += 32 * kConsumers * 4) {
-          const int col = at / kD, dim = at % kD, r = chunk * kNq + 8 * nt + col;
-          if (r >= rows) continue;
+          for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int pos = kFp8 ? 8 * g + 2 * mt + (e >> 1) : 16 * mt + g + 8 * (e >> 1);
+              obuf[(warp * 8 + 2 * q4 + (e & 1)) * kObufPitch + pos] =
+                  f[e & 1] == 0.f ? 0.f : o[4 * hh + mt][nt][e] * f[e & 1];
+            }
+          sm100::named_bar_sync(1, 32 * kConsumers);
+          // threads 0 .. 127: four dims of one row each
+          const int col = threadIdx.x >> 4, pos = (threadIdx.x & 15) * 4, r = chunk * kNq + 8 * nt + col;
+          if (col >= 8 || r >= rows) continue;
+          const int dim = kFp8 ? kD / 8 * (pos >> 3) + 8 * hh + (pos & 7) : 64 * hh + pos;
           float M = -INFINITY, den = 0.f;
 #pragma unroll
           for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, red_m[par][w][8 * nt + col]);
           float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < kConsumers; ++w) {
-            const float4 v = *reinterpret_cast<const float4*>(obuf + (w * 8 + col) * kLd + dim);
+            const float4 v = *reinterpret_cast<const float4*>(obuf + (w * 8 + col) * kObufPitch + pos);
             sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
             if (M != -INFINITY) den += red_l[par][w][8 * nt + col] * ex2(red_m[par][w][8 * nt + col] - M);
           }

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from gqa_util import ACT, Paged, check_fp8, check_out, check_turned, f64
+from gqa_util import quantise as _quantise
 from oracle import gqa
 
 pytestmark = pytest.mark.gpu
@@ -583,3 +584,36 @@ def test_a_layer_from_prompt_to_tokens(lib, act, kv, d, page, window, sink):
         check_out(got[:m], want, mag, zmag, act, f"prompt {b}")
         want, mag, zmag = gqa.attend(f64(tq[m:]), rows[0], rows[1], pos[m:], d ** -0.5, window, None if sk is None else f64(sk))
         check_out(got[m:], want, mag, zmag, act, f"tokens {b}")
+
+
+@pytest.mark.parametrize("kv", ["act", "fp8"])
+def test_decode_many_passes_over_a_large_cache(lib, kv):
+    """300 passes over a cache larger than L2, whose tiles arrive out of
+    order: every pass gives the same bits, and those of a plain softmax."""
+    B, n, H, G, d, page = 4, 40000, 16, 8, 128, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cols = -(-n // page)
+    k, v = (torch.randn((B * cols, G, page, d), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    table = torch.randperm(B * cols, generator=g, device="cuda").int().view(B, cols)
+    ks = vs = None
+    kf, vf = k.float(), v.float()
+    if kv == "fp8":
+        (k, ks), (v, vs) = ([x for x in _quantise(y)] for y in (kf, vf))
+        kf, vf = k.float() * ks[..., None], v.float() * vs[..., None]
+    q = torch.randn((B, H, d), generator=g, device="cuda").bfloat16()
+    p = _params(lib, "bf16", kv, B=B, n_heads=H, n_kv_heads=G, d=d, page=page, softmax_scale=0.1)
+    lens = [n, n - 1, n - 777, n // 2]
+    ws = torch.empty(lib.gqa_decode_attn_workspace_bytes(p, 1, n), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(q) for _ in range(2)]
+    err, lens_t, wrong = _err(), _i32(lens), torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(300):
+        lib.gqa_decode_attn(p, q, lib.make_gqa_cache(k, v, ks, vs), table, lens_t, 1, n, outs[min(i, 1)], ws, err=err)
+        if i:
+            wrong += (outs[0] != outs[1]).sum()
+    assert int(err[0]) == 0 and int(wrong) == 0
+    for b in range(B):
+        kk, vv = (x[table[b].long()].transpose(1, 2).reshape(-1, G, d)[:lens[b]].transpose(0, 1) for x in (kf, vf))
+        z = torch.einsum("ghd,gmd->ghm", q[b].float().view(G, H // G, d), kk) * 0.1
+        want = torch.softmax(z, -1) @ vv
+        # weights of tens of thousands of keys, each off by 2^-8 at most
+        assert (outs[0][b].float().view(G, H // G, d) - want).abs().max() < 2.0 ** -8 * (want.abs().max() + vv.abs().mean())
