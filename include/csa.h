@@ -458,7 +458,7 @@ typedef struct gqa_cache {
  * The turn is computed in fp32 (angles reduced in fp64).  CSA_KV_ACT rounds
  * the result once; CSA_KV_FP8 stores scale = amax/448 over the row's d values
  * (1 for a row of zeros) and the E4M3 codes of value / scale, both from the
- * fp32 result.  A token whose position is negative or past the table raises
+ * fp32 result; a row that holds a NaN or an infinity gets that as its scale.  A token whose position is negative or past the table raises
  * CSA_DEV_ERR_RANGE, one whose page is not in [0, n_pages) CSA_DEV_ERR_INDEX;
  * it is not stored (q_out and k_out are written all the same).  Two tokens
  * of one call must not share a cache slot. */
@@ -482,7 +482,8 @@ csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
  *   ws          workspace of gqa_decode_attn_workspace_bytes(params, T, n_max)
  * T is at most 64.  The keys of a page not in [0, n_pages) are skipped with
  * CSA_DEV_ERR_INDEX.  What masked slots hold (infinities and NaN included)
- * does not matter; logits of seen keys must be finite in fp32.  How a
+ * does not matter; logits of seen keys must be finite in fp32.  The
+ * scale of an FP8 value counts as no less than 2^-90 and no more than 2^90.  How a
  * sequence's keys are split depends on its own length, T and the window
  * alone, and partial results are joined in a fixed order: a query's output
  * is bit-identical run to run and whatever batch it is in. */

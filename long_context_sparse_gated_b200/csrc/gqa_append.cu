@@ -40,6 +40,13 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int B, int i) {
   return lo;
 }
 
+// The larger, or NaN if one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 template <bool kBf16, bool kFp8>
 __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const AppendArgs a) {
   __shared__ float cs[64], sn[64];
@@ -114,10 +121,10 @@ __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const AppendArgs a
     } else {
       float am = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(x[j]));
-      for (int o = pieces / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+      for (int j = 0; j < 8; ++j) am = max_nan(am, fabsf(x[j]));
+      for (int o = pieces / 2; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
       if (live && kind > 0 && page >= 0) {
-        const float scale = am > 0.f ? __fdiv_rn(am, kE4M3Max) : 1.f;
+        const float scale = am == 0.f ? 1.f : __fdiv_rn(am, kE4M3Max);  // NaN in a row: a NaN scale
         uint32_t w[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j / 4] |= f32_to_e4m3_sat(__fdiv_rn(x[j], scale)) << (8 * (j % 4));
