@@ -735,21 +735,20 @@ __global__ void __launch_bounds__(256) gqa_join_kernel(const DecodeArgs a) {
   for (int w = 0; w < 8; ++w) M = fmaxf(M, red_m[w]);
   constexpr int kV = kD / 32;
   float acc[kV] = {}, den = 0.f;
-  if (M != -INFINITY) {
+  const float mr = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
-    for (int s = warp; s < n; s += 8) {
-      const float2 ml = a.part_ml[slot + s * stride];
-      const float f = ex2(ml.x - M);
-      den = fmaf(ml.y, f, den);
-      const float* src = a.part_o + (slot + s * stride) * kD + kV * lane;
-      if (kV == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]);
-        acc[kV - 2] = fmaf(v.z, f, acc[kV - 2]); acc[kV - 1] = fmaf(v.w, f, acc[kV - 1]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]);
-      }
+  for (int s = warp; s < n; s += 8) {
+    const float2 ml = a.part_ml[slot + s * stride];
+    const float f = ex2(ml.x - mr);
+    den = fmaf(ml.y, f, den);
+    const float* src = a.part_o + (slot + s * stride) * kD + kV * lane;
+    if (kV == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]);
+      acc[kV - 2] = fmaf(v.z, f, acc[kV - 2]); acc[kV - 1] = fmaf(v.w, f, acc[kV - 1]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]);
     }
   }
 #pragma unroll

@@ -1,15 +1,49 @@
-// gqa_prompt_attn: causal attention over packed prompts.
+// gqa_prompt_attn: causal attention over packed prompts, on the 5th-generation
+// tensor cores.
 //
-// One warp per (query row, head) walks the row's keys with a running maximum
-// and sum; a lane holds d/32 dims of the query, the keys and the output.
+//   S = Q K^T,  P = exp(scale S - m),  O = P V / (exp(sink - m) + sum P)
+//
+// Work.  A unit is 128 query positions of one query head; units of a
+// sequence and KV head are numbered position tile by position tile, the heads
+// of a group inside, and a CTA takes two neighbours, which then mostly read
+// the same keys.  Blocks are ordered from a sequence's last positions (most
+// keys) to its first.
+//
+//   warp 8    loads: both Q tiles once, then K and V tiles of 128 keys into
+//             rings of their own (TMA, 128-byte swizzle)
+//   warp 9    issues the MMAs (tcgen05 kind::f16, M = 128, fp32 in TMEM):
+//             S_i = Q_i K^T from shared memory; O_i += P_i V with P_i read
+//             from TMEM, where it lies on top of S_i.  The two units take
+//             turns: while one's S is turned into P, the tensor cores run
+//             the other's products.
+//   warps 0-3, 4-7   softmax of unit 0 / 1, a thread a row: the row's 128
+//             logits in registers, running maximum, P in 16 bits back to
+//             TMEM.  The maximum moves only when a row exceeds it by 2^8, so
+//             O is hardly ever rescaled; at the end the same threads
+//             normalise O and write it out through shared memory.
+//   warp 10   looks through the value tiles that some row does not see as a
+//             whole.  Values that are not finite are taken out before the
+//             product (0 * NaN is NaN); where they belong to the sequence,
+//             and so to some of its rows, the units are computed again, row by row.
+//
+// TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d columns each).
+// Rounding: P to the activation type (relative 2^-9 or 2^-12); the rest fp32.
+#include <cuda.h>
+
 #include "gqa.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace csa {
 
 namespace {
 
 using namespace gqa;
+
+constexpr int kTile = 128;  // query positions of a unit, keys of a tile
+constexpr int kThreads = 384;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 8.f;  // base-2 units
 
 struct PromptArgs {
   gqa_rows q, k, v, out;
@@ -18,65 +52,500 @@ struct PromptArgs {
   const int32_t* cu_k;
   const float* sink;
   int B, n_heads, n_kv, window;
-  float scale;
+  float scale;  // softmax_scale * log2(e)
   int32_t* err;
 };
 
-template <bool kBf16, int kD>
-__device__ __forceinline__ void load_row(const gqa_rows& s, int64_t row, int h, int lane, float (&x)[kD / 32]) {
-  constexpr int n = kD / 32;
+template <int kD>
+struct __align__(1024) PromptSmem {
+  static constexpr int kOperand = kTile * kD * 2;
+  static constexpr int kK = kD == 128 ? 3 : 4, kV = kD == 128 ? 2 : 4;  // stages
+  uint8_t q[2][kOperand];  // later the staged output
+  uint8_t k[kK][kOperand];
+  uint8_t v[kV][kOperand];
+  uint64_t q_full, k_full[kK], k_empty[kK], v_full[kV], v_ok[kV], v_empty[kV];
+  uint64_t s_full[2], p_full[2], o_full;
+  uint32_t tmem;
+  int odd;
+  int abort;
+  int item[4];  // sequence, pair of units, KV head
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float (&r)[128], int at) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r) + at;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr)
+      : "memory");
+}
+// After tmem_ld_wait(): 32 registers count as produced here.
+__device__ __forceinline__ void pin32(float (&r)[128], int at) {
 #pragma unroll
-  for (int j = 0; j < n; j += 2) {
-    const float2 f = unpack2<kBf16>(*reinterpret_cast<const uint32_t*>(
-        reinterpret_cast<const uint16_t*>(s.ptr) + row * s.row_stride + h * s.head_stride + n * lane + j));
-    x[j] = f.x;
-    x[j + 1] = f.y;
+  for (int i = 0; i < 32; i += 8)
+    asm volatile(""
+                 : "+f"(r[at + i]), "+f"(r[at + i + 1]), "+f"(r[at + i + 2]), "+f"(r[at + i + 3]), "+f"(r[at + i + 4]),
+                   "+f"(r[at + i + 5]), "+f"(r[at + i + 6]), "+f"(r[at + i + 7]));
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&u)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
+      "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
+      "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// One unit: 128 positions of a query head.
+struct Unit {
+  int rows;        // its queries (0: no unit)
+  int head, row0;  // query head, first packed query row
+  int t0, t1;      // positions of its first and last query
+  int j0, j1;      // key tiles [j0, j1)
+};
+
+// The rows of a unit one by one, a warp a row: the path for values that are
+// not finite and belong to some of the rows.
+template <bool kBf16, int kD>
+__device__ __noinline__ void unit_by_rows(const PromptArgs& a, const Unit& u, int kvh, int k0, int warp, int lane) {
+  constexpr int n = kD / 32;
+  auto load = [&](const gqa_rows& s, int64_t row, int h, float (&x)[n]) {
+#pragma unroll
+    for (int j = 0; j < n; j += 2) {
+      const float2 f = unpack2<kBf16>(*reinterpret_cast<const uint32_t*>(
+          reinterpret_cast<const uint16_t*>(s.ptr) + row * s.row_stride + h * s.head_stride + n * lane + j));
+      x[j] = f.x;
+      x[j + 1] = f.y;
+    }
+  };
+  for (int r = warp; r < u.rows; r += 4) {
+    const int t = u.t0 + r, first = a.window > 0 ? max(0, t - a.window + 1) : 0;
+    float q[n], x[n], o[n] = {}, m = -INFINITY, l = 0.f;
+    load(a.q, u.row0 + r, u.head, q);
+    for (int j = first; j <= t; ++j) {
+      load(a.k, k0 + j, kvh, x);
+      float z = 0.f;
+#pragma unroll
+      for (int e = 0; e < n; ++e) z = fmaf(q[e], x[e], z);
+      z = warp_sum(z) * a.scale;
+      const float mn = fmaxf(m, z), f = m == -INFINITY ? 0.f : ex2(m - mn), p = ex2(z - mn);
+      load(a.v, k0 + j, kvh, x);
+      l = l * f + p;
+#pragma unroll
+      for (int e = 0; e < n; ++e) o[e] = fmaf(p, x[e], f == 0.f ? 0.f : o[e] * f);
+      m = mn;
+    }
+    if (a.sink && m != -INFINITY) l += ex2(a.sink[u.head] * kLog2e - m);
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < n; e += 2)
+      *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)(u.row0 + r) * a.out.row_stride +
+                                   u.head * a.out.head_stride + n * lane + e) = pack2<kBf16>(o[e] * inv, o[e + 1] * inv);
   }
 }
 
 template <bool kBf16, int kD>
-__global__ void __launch_bounds__(128) gqa_prompt_kernel(const PromptArgs a) {
-  constexpr int n = kD / 32;
+__global__ void __launch_bounds__(kThreads, 1)
+    gqa_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+  using Smem = PromptSmem<kD>;
+  extern __shared__ uint8_t raw[];
+  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &S.abort;
+
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (w >= (int64_t)a.n_q * a.n_heads) return;
-  const int row = (int)(w / a.n_heads), h = (int)(w % a.n_heads);
-  if (row >= a.cu_q[a.B]) return;
-  int lo = 0, hi = a.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.cu_q[mid] <= row) lo = mid; else hi = mid - 1;
-  }
-  const int q0 = a.cu_q[lo], q1 = a.cu_q[lo + 1], k0 = a.cu_k[lo], k1 = a.cu_k[lo + 1];
-  if (q0 < 0 || q1 > a.n_q || k0 < 0 || k1 > a.n_k || k1 < k0 || row < q0 || row >= q1) {
-    if (lane == 0) raise_err(a.err, CSA_DEV_ERR_RANGE);
-    return;
-  }
-  const int t = k1 - k0 - (q1 - q0) + (row - q0);
-  const int first = a.window > 0 ? max(0, t - a.window + 1) : 0;
-  const int kvh = h / (a.n_heads / a.n_kv);
-  float q[n], o[n] = {}, x[n];
-  load_row<kBf16, kD>(a.q, row, h, lane, q);
-  float m = a.sink ? a.sink[h] : -INFINITY, l = a.sink ? 1.f : 0.f;
-  for (int j = first; j <= t; ++j) {
-    load_row<kBf16, kD>(a.k, k0 + j, kvh, lane, x);
-    float z = 0.f;
+  // ---- which sequence, pair of units and KV head
+  const int G = a.n_heads / a.n_kv;
+  if (warp == 0) {
+    int base = 0, found = -1, rest = 0;
+    for (int b0 = 0; b0 < a.B && found < 0; b0 += 32) {
+      int n = 0;
+      if (b0 + lane < a.B) {
+        const int q0 = a.cu_q[b0 + lane], q1 = a.cu_q[b0 + lane + 1], k0 = a.cu_k[b0 + lane], k1 = a.cu_k[b0 + lane + 1];
+        if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k) {
+          if (blockIdx.x == 0) raise_err(a.err, CSA_DEV_ERR_RANGE);
+        } else {
+          n = ((q1 - q0 + kTile - 1) / kTile * G + 1) / 2 * a.n_kv;
+        }
+      }
+      int x = n;
 #pragma unroll
-    for (int e = 0; e < n; ++e) z = fmaf(q[e], x[e], z);
-    z = warp_sum(z) * a.scale;
-    const float mn = fmaxf(m, z), f = m == -INFINITY ? 0.f : expf(m - mn), p = expf(z - mn);
-    load_row<kBf16, kD>(a.v, k0 + j, kvh, lane, x);
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < n; ++e) o[e] = fmaf(p, x[e], o[e] * f);
-    m = mn;
+      for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const int at = (int)blockIdx.x - base - (x - n);
+      const unsigned hit = __ballot_sync(0xffffffffu, at >= 0 && at < n);
+      if (hit) {
+        found = b0 + __ffs(hit) - 1;
+        rest = __shfl_sync(0xffffffffu, at, __ffs(hit) - 1);
+      }
+      base += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) {
+      S.item[0] = found;
+      S.item[1] = rest;
+      S.odd = 0;
+      S.abort = 0;
+      sm100::mbar_init(&S.q_full, 1);
+      for (int i = 0; i < Smem::kK; ++i) {
+        sm100::mbar_init(&S.k_full[i], 1);
+        sm100::mbar_init(&S.k_empty[i], 1);
+      }
+      for (int i = 0; i < Smem::kV; ++i) {
+        sm100::mbar_init(&S.v_full[i], 1);
+        sm100::mbar_init(&S.v_ok[i], 1);
+        sm100::mbar_init(&S.v_empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        sm100::mbar_init(&S.s_full[i], 1);
+        sm100::mbar_init(&S.p_full[i], 4);
+      }
+      sm100::mbar_init(&S.o_full, 1);
+      sm100::fence_mbar_init();
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  __syncthreads();
+  const int b = S.item[0];
+  if (b < 0) return;
+  const int q_begin = a.cu_q[b], n_q = a.cu_q[b + 1] - q_begin, k_begin = a.cu_k[b], n_k = a.cu_k[b + 1] - k_begin;
+  const int tiles = (n_q + kTile - 1) / kTile, pairs = (tiles * G + 1) / 2;
+  const int kvh = S.item[1] % a.n_kv, pair = pairs - 1 - S.item[1] / a.n_kv;
+  Unit un[2];
 #pragma unroll
-  for (int e = 0; e < n; e += 2)
-    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out.ptr) + row * a.out.row_stride +
-                                 h * a.out.head_stride + n * lane + e) = pack2<kBf16>(o[e] * inv, o[e + 1] * inv);
+  for (int i = 0; i < 2; ++i) {
+    const int x = 2 * pair + i, tile = x / G;
+    Unit& u = un[i];
+    u.rows = tile < tiles ? min(kTile, n_q - tile * kTile) : 0;
+    u.head = kvh * G + x % G;
+    u.row0 = q_begin + tile * kTile;
+    u.t0 = n_k - n_q + tile * kTile;
+    u.t1 = u.rows > 0 ? u.t0 + u.rows - 1 : -1;
+    const bool some = u.rows > 0 && u.t1 >= 0;
+    u.j0 = some && a.window > 0 ? max(0, u.t0 - a.window + 1) / kTile : 0;
+    u.j1 = some ? u.t1 / kTile + 1 : u.j0;
+  }
+  const int work0 = un[0].j1 - un[0].j0, work1 = un[1].j1 - un[1].j0;
+  const int j_begin = work0 == 0 ? un[1].j0 : (work1 == 0 ? un[0].j0 : min(un[0].j0, un[1].j0));
+  const int j_end = work0 == 0 ? un[1].j1 : (work1 == 0 ? un[0].j1 : max(un[0].j1, un[1].j1));
+  // a tile that some row of the unit does not see as a whole
+  auto edge_of = [&](const Unit& u, int j) {
+    return j >= u.j0 && j < u.j1 && (j * kTile + kTile - 1 > u.t0 || (a.window > 0 && j * kTile <= u.t1 - a.window));
+  };
+
+  if (warp == 8) {
+    sm100::tmem_alloc(&S.tmem, 512);
+    sm100::tmem_relinquish();
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = S.tmem;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8 && lane == 0) {
+      // ---- loads
+      int n_live = (work0 > 0) + (work1 > 0);
+      if (n_live) sm100::mbar_arrive_expect_tx(&S.q_full, n_live * Smem::kOperand);
+      for (int i = 0; i < 2; ++i)
+        if ((i ? work1 : work0) > 0)
+          for (int c = 0; c < kD / 64; ++c)
+            sm100::tma_load_3d(S.q[i] + c * kTile * 128, &map_q, &S.q_full, 64 * c, un[i].row0, un[i].head);
+      int n = 0;
+      for (int j = j_begin; j < j_end; ++j, ++n) {
+        const int ks = n % Smem::kK, vs = n % Smem::kV;
+        if (n >= Smem::kK) sm100::mbar_wait(&S.k_empty[ks], (n / Smem::kK - 1) & 1, abort);
+        if (*abort) break;
+        sm100::mbar_arrive_expect_tx(&S.k_full[ks], Smem::kOperand);
+        for (int c = 0; c < kD / 64; ++c)
+          sm100::tma_load_3d(S.k[ks] + c * kTile * 128, &map_k, &S.k_full[ks], 64 * c, k_begin + j * kTile, kvh);
+        if (n >= Smem::kV) sm100::mbar_wait(&S.v_empty[vs], (n / Smem::kV - 1) & 1, abort);
+        if (*abort) {
+          ++n;
+          break;
+        }
+        sm100::mbar_arrive_expect_tx(&S.v_full[vs], Smem::kOperand);
+        for (int c = 0; c < kD / 64; ++c)
+          sm100::tma_load_3d(S.v[vs] + c * kTile * 128, &map_v, &S.v_full[vs], 64 * c, k_begin + j * kTile, kvh);
+      }
+      if (*abort) {
+        // copies in flight land before the CTA goes (each wait bounded)
+        auto drain = [&](uint64_t* bar, int parity) {
+          const uint64_t t0 = sm100::globaltimer();
+          while (!sm100::mbar_try_wait(bar, parity) && sm100::globaltimer() - t0 < sm100::kWaitNs) {
+          }
+        };
+        if (n_live) drain(&S.q_full, 0);
+        for (int i = max(0, n - Smem::kK); i < n; ++i) drain(&S.k_full[i % Smem::kK], (i / Smem::kK) & 1);
+        for (int i = max(0, n - Smem::kV); i < n; ++i) drain(&S.v_full[i % Smem::kV], (i / Smem::kV) & 1);
+      }
+    } else if (warp == 9 && lane == 0) {
+      // ---- MMAs
+      const uint32_t id_s = kBf16 ? sm100::idesc_bf16(kTile, kTile, 0, 0) : sm100::idesc_f16(kTile, kTile, 0, 0);
+      const uint32_t id_o = kBf16 ? sm100::idesc_bf16(kTile, kD, 0, 1) : sm100::idesc_f16(kTile, kD, 0, 1);
+      // Q and K K-major (8-row groups 1 KB apart, 64-dim halves 16 KB); V
+      // MN-major: 64-dim halves 16 KB apart, groups of 8 keys 1 KB
+      uint64_t dq[2], dk[Smem::kK], dv[Smem::kV];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) dq[i] = sm100::smem_desc(sm100::smem_u32(S.q[i]), 16, 1024, 2);
+#pragma unroll
+      for (int i = 0; i < Smem::kK; ++i) dk[i] = sm100::smem_desc(sm100::smem_u32(S.k[i]), 16, 1024, 2);
+#pragma unroll
+      for (int i = 0; i < Smem::kV; ++i) dv[i] = sm100::smem_desc(sm100::smem_u32(S.v[i]), kTile * 128, 1024, 2);
+      const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 256 + kD};
+      auto active = [&](int i, int j) { return j >= un[i].j0 && j < un[i].j1; };
+      auto issue_s = [&](int i, int n) {  // S_i = Q_i K^T with the n-th K tile
+        sm100::tc_fence_after();
+        if (!*abort) {
+          uint64_t k = dk[0];
+#pragma unroll
+          for (int x = 1; x < Smem::kK; ++x)
+            if (n % Smem::kK == x) k = dk[x];
+          const uint64_t q = i ? dq[1] : dq[0];
+#pragma unroll
+          for (int c = 0; c < kD / 16; ++c) {
+            const uint32_t off = ((c >> 2) * kTile * 128 + (c & 3) * 32) >> 4;
+            sm100::mma_f16(i ? s_col[1] : s_col[0], q + off, k + off, id_s, c > 0);
+          }
+        }
+        sm100::tc_commit(&S.s_full[i]);
+      };
+      if (j_begin < j_end) {
+        sm100::mbar_wait_poll(&S.q_full, 0, abort);
+        sm100::mbar_wait_poll(&S.k_full[0], 0, abort);
+        for (int i = 0; i < 2; ++i)
+          if (active(i, j_begin)) issue_s(i, 0);
+        sm100::tc_commit(&S.k_empty[0]);
+      }
+      int done[2] = {0, 0};
+      for (int j = j_begin, n = 0; j < j_end; ++j, ++n) {
+        const int vs = n % Smem::kV;
+        sm100::mbar_wait_poll(&S.v_ok[vs], (n / Smem::kV) & 1, abort);
+        if (j + 1 < j_end) sm100::mbar_wait_poll(&S.k_full[(n + 1) % Smem::kK], ((n + 1) / Smem::kK) & 1, abort);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (active(i, j)) {
+            sm100::mbar_wait_poll(&S.p_full[i], done[i] & 1, abort);
+            sm100::tc_fence_after();
+            if (!*abort) {
+              uint64_t v = dv[0];
+#pragma unroll
+              for (int x = 1; x < Smem::kV; ++x)
+                if (vs == x) v = dv[x];
+#pragma unroll
+              for (int c = 0; c < kTile / 16; ++c)
+                mma_f16_ts(o_col[i], s_col[i] + 8 * c, v + ((c * 2048) >> 4), id_o, (done[i] > 0 || c > 0) ? 1u : 0u);
+            }
+            ++done[i];
+          }
+          if (active(i, j + 1)) issue_s(i, n + 1);
+        }
+        sm100::tc_commit(&S.v_empty[vs]);
+        if (j + 1 < j_end) sm100::tc_commit(&S.k_empty[(n + 1) % Smem::kK]);
+      }
+      sm100::tc_commit(&S.o_full);
+      if (*abort) {
+        const uint64_t t0 = sm100::globaltimer();
+        while (!sm100::mbar_try_wait(&S.o_full, 0) && sm100::globaltimer() - t0 < sm100::kWaitNs) {
+        }
+      }
+    } else if (warp == 10) {
+      // ---- values that are not finite
+      for (int j = j_begin, n = 0; j < j_end; ++j, ++n) {
+        const int vs = n % Smem::kV;
+        sm100::mbar_wait(&S.v_full[vs], (n / Smem::kV) & 1, abort);
+        if (edge_of(un[0], j) || edge_of(un[1], j)) {
+          constexpr uint32_t e = kBf16 ? 0x7F80u : 0x7C00u;
+          bool own = false, any = false;
+          uint4* v4 = reinterpret_cast<uint4*>(S.v[vs]);
+#pragma unroll 4
+          for (int x = lane; x < Smem::kOperand / 16; x += 32) {
+            uint4 w = v4[x];
+            uint32_t bad[4];
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            uint32_t some = 0;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              bad[y] = ((in[y] & e) == e ? 0xFFFFu : 0u) | ((in[y] & (e << 16)) == (e << 16) ? 0xFFFF0000u : 0u);
+              some |= bad[y];
+            }
+            if (some) {
+              v4[x] = make_uint4(w.x & ~bad[0], w.y & ~bad[1], w.z & ~bad[2], w.w & ~bad[3]);
+              any = true;
+              own |= j * kTile + ((x >> 3) & (kTile - 1)) <= max(un[0].t1, un[1].t1);  // a key that some row may see
+            }
+          }
+          if (own) S.odd = 1;
+          if (any) sm100::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) sm100::mbar_arrive(&S.v_ok[vs]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---- softmax: unit i, row r
+    const int i = warp >> 2, r = (warp & 3) * 32 + lane;
+    const Unit u = i ? un[1] : un[0];
+    const int work = i ? work1 : work0;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + 128 * i + lanes, o_col = tmem + 256 + kD * i + lanes;
+    const int t = u.t0 + r;
+    float m = -INFINITY, l = 0.f;  // m in units of S
+    const float step = kLazy / a.scale;
+    for (int n = 0; n < work; ++n) {
+      const int key0 = (u.j0 + n) * kTile;
+      float s[128];
+      sm100::mbar_wait(&S.s_full[i], n & 1, abort);
+      sm100::tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) tmem_ld_x32(s_col + c, s, c);
+      sm100::tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) pin32(s, c);
+      if (edge_of(u, u.j0 + n)) {
+        const int hi = t - key0, lo = a.window > 0 ? t - a.window - key0 : INT32_MIN;  // seen: lo < c <= hi
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > hi || c <= lo) s[c] = -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < 128; c += 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const bool over = top > m + step;
+      if (__any_sync(0xffffffffu, over)) {
+        const float alpha = over ? ex2((m - top) * a.scale) : 1.f;  // 0 from -inf
+        if (over) m = top;
+        l *= alpha;
+        if (n > 0) {
+          // S being here says that the products before it are done
+#pragma unroll
+          for (int c = 0; c < kD; c += 16) {
+            uint32_t w[16];
+            sm100::tmem_ld_x16(o_col + c, w);
+            sm100::tmem_ld_wait();
+            sm100::tmem_pin16(w);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+            sm100::tmem_st_x16(o_col + c, w);
+          }
+        }
+      }
+      const float mc = m == -INFINITY ? 0.f : m * a.scale;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t p[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float x = ex2(fmaf(s[64 * half + 2 * c], a.scale, -mc)), y = ex2(fmaf(s[64 * half + 2 * c + 1], a.scale, -mc));
+          sum[(2 * c) & 3] += x;
+          sum[(2 * c + 1) & 3] += y;
+          p[c] = pack2<kBf16>(x, y);
+        }
+        tmem_st_x32(s_col + 32 * half, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      sm100::tmem_st_wait();
+      sm100::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&S.p_full[i]);
+    }
+
+    // ---- output
+    if (work > 0) {
+      sm100::mbar_wait(&S.o_full, 0, abort);
+      sm100::tc_fence_after();
+    }
+    if (u.rows > 0) {
+      if (a.sink && m != -INFINITY) l += ex2(a.sink[u.head] * kLog2e - m * a.scale);
+      const float f = l != 0.f ? 1.f / l : 0.f;
+      constexpr int kChunks = kD / 8;  // 16-byte pieces of a row
+      uint4* stage = reinterpret_cast<uint4*>(S.q[i]) + (warp & 3) * 32 * kChunks;  // the warp's 32 rows
+#pragma unroll
+      for (int c = 0; c < kD; c += 16) {
+        uint32_t w[16];
+        if (work > 0) {
+          sm100::tmem_ld_x16(o_col + c, w);
+          sm100::tmem_ld_wait();
+          sm100::tmem_pin16(w);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = 0;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[8 * h + e]) * f;
+          stage[lane * kChunks + ((c / 8 + h) ^ (lane & 7))] = pack8<kBf16>(x);
+        }
+      }
+      __syncwarp();
+      if (!*abort) {
+#pragma unroll
+        for (int x = lane; x < 32 * kChunks; x += 32) {
+          const int row = x / kChunks, ch = x % kChunks;
+          if ((warp & 3) * 32 + row < u.rows) {
+            uint16_t* dst = reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)(u.row0 + (warp & 3) * 32 + row) * a.out.row_stride +
+                            (int64_t)u.head * a.out.head_stride + 8 * ch;
+            *reinterpret_cast<uint4*>(dst) = stage[row * kChunks + (ch ^ (row & 7))];
+          }
+        }
+        if (*reinterpret_cast<volatile int*>(&S.odd)) {
+          // all four warps have written their rows before others rewrite them
+          sm100::named_bar_sync(1 + i, 128);
+          unit_by_rows<kBf16, kD>(a, u, kvh, k_begin, warp & 3, lane);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (S.abort && threadIdx.x == 0) raise_err(a.err, CSA_DEV_ERR_TIMEOUT);
+  if (warp == 8) {
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc(tmem, 512);
+  }
+  pdl_trigger();
+}
+
+template <bool kBf16, int kD>
+cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptArgs& a, int64_t blocks,
+                   cudaStream_t st) {
+  auto fn = gqa_prompt_kernel<kBf16, kD>;
+  const size_t smem = sizeof(PromptSmem<kD>) + 1024;
+  static_assert(sizeof(PromptSmem<kD>) + 1024 <= 232448, "shared memory of a CTA");
+  const cudaError_t e = set_max_smem(reinterpret_cast<const void*>(fn), smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fn, dim3((unsigned)blocks), dim3(kThreads), smem, st, mq, mk, mv, a);
 }
 
 }  // namespace
@@ -84,13 +553,27 @@ __global__ void __launch_bounds__(128) gqa_prompt_kernel(const PromptArgs a) {
 cudaError_t launch_gqa_prompt(const gqa_params& p, const gqa_rows& q, const gqa_rows& k, const gqa_rows& v,
                               int64_t n_q, int64_t n_k, const int32_t* cu_q, const int32_t* cu_k, const float* sink,
                               const gqa_rows& out, int32_t* err, cudaStream_t st) {
-  const PromptArgs a{q, k, v, out, (int)n_q, (int)n_k, cu_q, cu_k, sink,
-                     p.B, p.n_heads, p.n_kv_heads, p.window, p.softmax_scale, err};
   const bool bf = p.act_fmt == CSA_ACT_BF16;
-  auto fn = bf ? (p.d == 128 ? gqa_prompt_kernel<true, 128> : gqa_prompt_kernel<true, 64>)
-               : (p.d == 128 ? gqa_prompt_kernel<false, 128> : gqa_prompt_kernel<false, 64>);
-  const int64_t warps = n_q * p.n_heads;
-  return launch_pdl(fn, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, a);
+  const CUtensorMapDataType dt = bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  auto encode = [&](CUtensorMap* m, const gqa_rows& x, int64_t rows, int heads) {
+    const uint64_t dims[3] = {(uint64_t)p.d, (uint64_t)rows, (uint64_t)heads};
+    const uint64_t str[2] = {(uint64_t)x.row_stride * 2, (uint64_t)x.head_stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)kTile, 1};
+    return encode_tensor_map(m, dt, 3, x.ptr, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  CUtensorMap mq, mk, mv;
+  // without keys nothing is loaded: the queries' map stands in
+  if (!encode(&mq, q, n_q, p.n_heads) || !encode(&mk, n_k ? k : q, n_k ? n_k : n_q, n_k ? p.n_kv_heads : p.n_heads) ||
+      !encode(&mv, n_k ? v : q, n_k ? n_k : n_q, n_k ? p.n_kv_heads : p.n_heads))
+    return cudaErrorInvalidValue;
+  const PromptArgs a{q, k, v, out, (int)n_q, (int)n_k, cu_q, cu_k, sink,
+                     p.B, p.n_heads, p.n_kv_heads, p.window, p.softmax_scale * kLog2e, err};
+  // the most pairs of units that B sequences of n_q queries can have
+  const int64_t G = p.n_heads / p.n_kv_heads, tiles = n_q / kTile + (n_q < p.B ? n_q : p.B);
+  const int64_t blocks = (tiles * G + p.B + 1) / 2 * p.n_kv_heads;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  return bf ? (p.d == 128 ? launch<true, 128>(mq, mk, mv, a, blocks, st) : launch<true, 64>(mq, mk, mv, a, blocks, st))
+            : (p.d == 128 ? launch<false, 128>(mq, mk, mv, a, blocks, st) : launch<false, 64>(mq, mk, mv, a, blocks, st));
 }
 
 }  // namespace csa
