@@ -177,7 +177,10 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        try:  # the handle of torch.cuda.current_stream() without the object around it (3 us a call)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -327,19 +330,28 @@ def make_gqa_cache(k, v, k_scale=None, v_scale=None) -> GqaCache:
 
 
 _NO_ROWS = GqaRows(None, 0, 0)
-_ACT_DTYPES = {ACT_BF16: "torch.bfloat16", ACT_F16: "torch.float16"}
 
 
-def _rows(x, params, heads):
+def _gqa_types(params):
+    """(torch dtype of act_fmt, current device) that every row tensor has to
+    match: kernels are launched on the current device."""
+    import torch
+    return torch.bfloat16 if params.act_fmt == ACT_BF16 else torch.float16, torch._C._cuda_getDevice()
+
+
+def _rows(x, types, heads, d):
     """gqa_rows of a CUDA tensor [n, heads, d] of the activation type; only
     its last dim has to be contiguous."""
-    if not x.is_cuda:
-        raise TypeError("libcsa takes CUDA tensors (device pointers); got a host array")
-    if str(x.dtype) != _ACT_DTYPES.get(params.act_fmt, str(x.dtype)):
-        raise TypeError(f"act_fmt says {_ACT_DTYPES[params.act_fmt]}, got {x.dtype}")
-    n, h, d = x.shape
-    if h != heads or d != params.d:
-        raise ValueError(f"expected [n, {heads}, {params.d}], got {tuple(x.shape)}")
+    dtype, device = types
+    if x.get_device() != device:
+        if not x.is_cuda:
+            raise TypeError("libcsa takes CUDA tensors (device pointers); got a host array")
+        raise ValueError(f"tensor on device {x.get_device()}, but device {device} is current")
+    if x.dtype is not dtype:
+        raise TypeError(f"act_fmt says {dtype}, got {x.dtype}")
+    n, h, last = x.shape
+    if h != heads or last != d:
+        raise ValueError(f"expected [n, {heads}, {d}], got {tuple(x.shape)}")
     sn, sh, sd = x.stride()
     if sd != 1:
         raise ValueError("the last dim of a row tensor has to be contiguous")
@@ -356,15 +368,17 @@ def gqa_cache_append(params, q, k, v, cu, pos0, cache, table, q_out=None, k_out=
     ``cache`` through ``table`` ([B, cols]), keys turned by their positions.
     Turned queries (``q`` [n, n_heads, d], or None) go to ``q_out``, turned
     keys to ``k_out`` (both may be the inputs)."""
-    hk = params.n_kv_heads
-    if v.shape[0] != k.shape[0] or any(x is not None and x.shape[0] != k.shape[0] for x in (q, q_out, k_out)):
-        raise ValueError("q, k, v, q_out and k_out have the same rows")
+    n, d, hk, hq = k.shape[0], params.d, params.n_kv_heads, params.n_heads
+    for x in (v, q, q_out, k_out):
+        if x is not None and x.shape[0] != n:
+            raise ValueError("q, k, v, q_out and k_out have the same rows")
+    ty = _gqa_types(params) if k.is_cuda else (k.dtype, None)
     st = lib().gqa_cache_append(
-        ctypes.byref(params), _NO_ROWS if q is None else _rows(q, params, params.n_heads), _rows(k, params, hk),
-        _rows(v, params, hk), k.shape[0], _ptr(cu), _ptr(pos0), cache, _ptr(table), table.shape[1],
-        _NO_ROWS if q_out is None else _rows(q_out, params, params.n_heads),
-        _NO_ROWS if k_out is None else _rows(k_out, params, hk), _ptr(err), _stream(stream))
-    _check("gqa_cache_append", st)
+        ctypes.byref(params), _NO_ROWS if q is None else _rows(q, ty, hq, d), _rows(k, ty, hk, d), _rows(v, ty, hk, d), n,
+        _ptr(cu), _ptr(pos0), cache, _ptr(table), table.shape[1], _NO_ROWS if q_out is None else _rows(q_out, ty, hq, d),
+        _NO_ROWS if k_out is None else _rows(k_out, ty, hk, d), _ptr(err), _stream(stream))
+    if st:
+        _check("gqa_cache_append", st)
 
 
 def gqa_decode_attn_workspace_bytes(params, T, n_max):
@@ -377,11 +391,13 @@ def gqa_decode_attn(params, q, cache, table, lens, T, n_max, out, ws=None, sink=
     CUDA byte tensor of gqa_decode_attn_workspace_bytes(params, T, n_max)."""
     if q.shape[0] != params.B * T or out.shape[0] != params.B * T:
         raise ValueError("q and out have B * T rows")
+    ty = _gqa_types(params) if q.is_cuda else (q.dtype, None)
+    hq, d = params.n_heads, params.d
     st = lib().gqa_decode_attn(
-        ctypes.byref(params), _rows(q, params, params.n_heads), cache, _ptr(table), table.shape[1], _ptr(lens), T,
-        n_max, _ptr(sink), _rows(out, params, params.n_heads), _ptr(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _ptr(err), _stream(stream))
-    _check("gqa_decode_attn", st)
+        ctypes.byref(params), _rows(q, ty, hq, d), cache, _ptr(table), table.shape[1], _ptr(lens), T, n_max, _ptr(sink),
+        _rows(out, ty, hq, d), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(err), _stream(stream))
+    if st:
+        _check("gqa_decode_attn", st)
 
 
 def gqa_prompt_attn(params, q, k, v, cu_q, cu_k, out, sink=None, err=None, stream=None):
@@ -391,9 +407,10 @@ def gqa_prompt_attn(params, q, k, v, cu_q, cu_k, out, sink=None, err=None, strea
     n_kv_heads, d]); the last query sits at the last key."""
     if out.shape[0] != q.shape[0] or v.shape[0] != k.shape[0]:
         raise ValueError("q and out have the same rows, and k and v")
-    hk = params.n_kv_heads
+    ty = _gqa_types(params) if q.is_cuda else (q.dtype, None)
+    hk, hq, d = params.n_kv_heads, params.n_heads, params.d
     st = lib().gqa_prompt_attn(
-        ctypes.byref(params), _rows(q, params, params.n_heads), _rows(k, params, hk), _rows(v, params, hk),
-        q.shape[0], k.shape[0], _ptr(cu_q), _ptr(cu_k), _ptr(sink), _rows(out, params, params.n_heads), _ptr(err),
-        _stream(stream))
-    _check("gqa_prompt_attn", st)
+        ctypes.byref(params), _rows(q, ty, hq, d), _rows(k, ty, hk, d), _rows(v, ty, hk, d), q.shape[0], k.shape[0],
+        _ptr(cu_q), _ptr(cu_k), _ptr(sink), _rows(out, ty, hq, d), _ptr(err), _stream(stream))
+    if st:
+        _check("gqa_prompt_attn", st)

@@ -1,10 +1,24 @@
 // gqa_cache_append: new tokens' keys and values into the paged cache, keys
 // and queries turned by their positions on the way.
 //
-// One CTA per token.  The token's cosines and sines (one pair per rotated
-// pair of dims, shared by all heads) go to shared memory once; a thread then
-// carries 8 dims (16 bytes in) of one head at a time through the turn to all
-// the places they are written to.
+// Bound by bytes (each row read once, written once or twice), and by latency
+// for a decode step.  A CTA takes one token, or several while their rows are
+// few; a thread carries 8 dims (16 bytes in) of a head at a time.  The rows'
+// addresses do not depend on positions, so the first four loads of a thread
+// are on their way before one warp per token looks up its sequence, position
+// and page and fills the token's cosines and sines (one pair per rotated pair
+// of dims, shared by all heads) in shared memory.
+//
+// Angles.  pos * theta^(-2j/r) in turns: the frequencies / 2 pi come from the
+// host in fp64, the product is reduced to [-1/2, 1/2] turns in fp64 and only
+// then rounded, so that an angle is off by 2^-25 turns at any position.
+//
+// FP8.  The lanes that hold a row agree on its largest magnitude; codes are
+// those of value * (1 / scale), which differs from value / scale by an fp32
+// rounding (a code differs only where the quotient is that near a border).
+#include <cmath>
+#include <cstring>
+
 #include "gqa.cuh"
 #include "kernels.h"
 
@@ -15,30 +29,26 @@ namespace {
 using namespace gqa;
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 2;     // pieces of 16 dims that a thread has in flight
+constexpr int kMaxTokens = 8; // per CTA, a warp each
 
 struct AppendArgs {
-  gqa_rows q, k, v, q_out, k_out;
-  gqa_cache cache;
+  gqa_rows in[3];   // q, k, v
+  gqa_rows out[2];  // q_out, k_out
+  void* cache[3];   // -, k, v
+  float* scale[3];
+  int64_t n_pages;
   const int32_t* cu;
   const int32_t* pos0;
   const int32_t* table;
   int64_t table_cols;
-  int B, n_heads, n_kv, d, r, page;
-  float theta;
+  int n_tokens, tokens;  // all, per CTA
+  int B, nq, n_kv, r, page, page_shift;
+  int rows, per_token;   // rows (heads) of a CTA, of a token
+  uint32_t token_magic;  // ceil(2^16 / per_token), with several tokens per CTA
   int32_t* err;
+  double turns[64];  // theta^(-2j/r) / 2 pi
 };
-
-// The sequence that packed row i belongs to: the last b with cu[b] <= i (so
-// that empty sequences are passed over), or -1 when i >= cu[B].
-__device__ __forceinline__ int find_seq(const int32_t* cu, int B, int i) {
-  if (i >= cu[B]) return -1;
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu[mid] <= i) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
 
 // The larger, or NaN if one of them is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -47,92 +57,182 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-template <bool kBf16, bool kFp8>
-__global__ void __launch_bounds__(kThreads) gqa_append_kernel(const AppendArgs a) {
-  __shared__ float cs[64], sn[64];
+// The sequence that packed row i belongs to: the last b with cu[b] <= i (so
+// that empty sequences are passed over), or -1 when i >= cu[B].  A warp
+// narrows 32 ways at a time.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int B, int i, int lane) {
+  int lo = 0, n = B + 1;  // cu[lo] <= i, and it is one of cu[lo .. lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool le = lane * step < n && cu[at] <= i;
+    const unsigned hits = __ballot_sync(0xffffffffu, le) | 1u;
+    const int last = 31 - __clz(hits);
+    n = min(step, n - last * step);
+    lo += last * step;
+  }
+  return lo < B ? lo : -1;
+}
+
+template <bool kBf16, bool kFp8, int kD>
+__global__ void __launch_bounds__(kThreads) gqa_append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kPieces = kD / 16;  // of a row: 8 or 4 neighbouring lanes
+  __shared__ __align__(16) float2 turn[kMaxTokens][kD / 2];
+  __shared__ int64_t row0[kMaxTokens];  // page * n_kv * page size + slot, -1: not stored, -2: no token
   pdl_wait();
-  const int i = blockIdx.x;
-  const int b = find_seq(a.cu, a.B, i);
-  if (b < 0) return;
-  const int64_t pos = (int64_t)a.pos0[b] + (i - a.cu[b]);
-  const int half = a.r / 2;
-  if ((int)threadIdx.x < half) {
-    float c, s;
-    rope_cos_sin((double)pos, threadIdx.x, a.r, (double)a.theta, &c, &s);
-    cs[threadIdx.x] = c;
-    sn[threadIdx.x] = s;
+  const int i0 = blockIdx.x * a.tokens;
+  const int c = threadIdx.x % kPieces;
+  const int pair0 = 8 * c - (kD - a.r) / 2;  // first of this thread's pairs
+  constexpr int kRows = kThreads / kPieces;  // rows that the CTA's threads cover at once
+
+  // A row of the CTA: its token and kind (0 q, 1 k, 2 v), and the head.
+  auto locate = [&](int row, int& tok, int& kind, int& h) {
+    tok = a.tokens > 1 ? (int)((uint32_t)row * a.token_magic >> 16) : 0;
+    h = row - tok * a.per_token;
+    kind = 0;
+    if (h >= a.nq) {
+      h -= a.nq;
+      kind = h >= a.n_kv ? 2 : 1;
+      h -= h >= a.n_kv ? a.n_kv : 0;
+    }
+  };
+  uint4 w[kBatch][2];
+  auto load = [&](int k, int row) {
+    int tok, kind, h;
+    locate(row, tok, kind, h);
+    w[k][0] = w[k][1] = make_uint4(0, 0, 0, 0);
+    if (row >= a.rows || i0 + tok >= a.n_tokens) return;
+    const gqa_rows& s = a.in[kind];
+    const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(s.ptr) + (i0 + tok) * s.row_stride +
+                                                      h * s.head_stride + 16 * c);
+    w[k][0] = src[0];
+    w[k][1] = src[1];
+  };
+  const int row_t = threadIdx.x / kPieces;
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) load(k, row_t + k * kRows);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < a.tokens) {
+    const int i = i0 + warp;
+    const int b = i < a.n_tokens ? find_seq(a.cu, a.B, i, lane) : -1;
+    int64_t at = -2;
+    if (b >= 0) {
+      const int64_t pos = (int64_t)a.pos0[b] + (i - a.cu[b]);
+      for (int j = lane; 2 * j < a.r; j += 32) {
+        double t = (double)pos * a.turns[j];
+        t -= rint(t);
+        float s, co;
+        sincospif(2.f * (float)t, &s, &co);
+        turn[warp][j] = make_float2(co, s);
+      }
+      at = -1;
+      if (pos < 0 || pos >= a.table_cols << a.page_shift) {
+        if (lane == 0) raise_err(a.err, CSA_DEV_ERR_RANGE);
+      } else {
+        const int64_t id = a.table[(int64_t)b * a.table_cols + (pos >> a.page_shift)];
+        if (id < 0 || id >= a.n_pages) {
+          if (lane == 0) raise_err(a.err, CSA_DEV_ERR_INDEX);
+        } else {
+          at = (id * a.n_kv << a.page_shift) + (pos & (a.page - 1));
+        }
+      }
+    }
+    if (lane == 0) row0[warp] = at;
   }
   __syncthreads();
-  int64_t page = -1;
-  int slot = 0;
-  if (pos < 0 || pos >= a.table_cols * a.page) {
-    if (threadIdx.x == 0) raise_err(a.err, CSA_DEV_ERR_RANGE);
-  } else {
-    page = a.table[(int64_t)b * a.table_cols + pos / a.page];
-    slot = (int)(pos % a.page);
-    if (page < 0 || page >= a.cache.n_pages) {
-      if (threadIdx.x == 0) raise_err(a.err, CSA_DEV_ERR_INDEX);
-      page = -1;
+
+  // whole warps stay for the shuffles
+  constexpr int kWarpRows = 32 / kPieces;
+  const int rows_up = (a.rows + kWarpRows - 1) / kWarpRows * kWarpRows;
+  for (int row0_t = row_t; row0_t < rows_up; row0_t += kBatch * kRows) {
+    if (row0_t != row_t) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) load(k, row0_t + k * kRows);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int row = row0_t + k * kRows;
+      if (row >= rows_up) break;
+      int tok, kind, h;
+      locate(min(row, a.rows - 1), tok, kind, h);
+      const int64_t at = row < a.rows ? row0[tok] : -2;
+      float v[2][8];
+      unpack8<kBf16>(w[k][0], v[0]);
+      unpack8<kBf16>(w[k][1], v[1]);
+      if (kind < 2) {
+        // r is a multiple of 8: the rotated dims begin at either half
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (pair0 + 4 * e < 0) continue;
+          const float4* t4 = reinterpret_cast<const float4*>(&turn[tok][pair0 + 4 * e]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float4 t = t4[j];  // (cos, sin) of two pairs
+            const float p = v[e][4 * j], q = v[e][4 * j + 1], x = v[e][4 * j + 2], y = v[e][4 * j + 3];
+            v[e][4 * j] = fmaf(p, t.x, -(q * t.y));
+            v[e][4 * j + 1] = fmaf(p, t.y, q * t.x);
+            v[e][4 * j + 2] = fmaf(x, t.z, -(y * t.w));
+            v[e][4 * j + 3] = fmaf(x, t.w, y * t.z);
+          }
+        }
+        w[k][0] = pack8<kBf16>(v[0]);
+        w[k][1] = pack8<kBf16>(v[1]);
+        const gqa_rows& dst = a.out[kind];
+        if (at >= -1 && dst.ptr) {
+          uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(dst.ptr) + (i0 + tok) * dst.row_stride +
+                                               h * dst.head_stride + 16 * c);
+          to[0] = w[k][0];
+          to[1] = w[k][1];
+        }
+      }
+      const int64_t slot = at + ((int64_t)h << a.page_shift);
+      if (!kFp8) {
+        if (at >= 0 && kind > 0) {
+          uint4* to = reinterpret_cast<uint4*>(a.cache[kind]) + (slot * kPieces + c) * 2;
+          to[0] = w[k][0];
+          to[1] = w[k][1];
+        }
+      } else if (__any_sync(0xffffffffu, kind > 0)) {
+        float am = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) am = max_nan(am, fabsf(v[j / 8][j % 8]));
+#pragma unroll
+        for (int o = kPieces / 2; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
+        if (at >= 0 && kind > 0) {
+          const float scale = am == 0.f ? 1.f : __fdiv_rn(am, kE4M3Max);  // NaN in a row: a NaN scale
+          // a reciprocal beyond fp32 (rows below 2^-117): divide
+          const float inv = __frcp_rn(scale);
+          const bool tiny = !(inv < INFINITY);
+          uint32_t u[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float x = v[j / 4][2 * (j % 4)], y = v[j / 4][2 * (j % 4) + 1];
+            const float2 z = tiny ? make_float2(__fdiv_rn(x, scale), __fdiv_rn(y, scale)) : make_float2(x * inv, y * inv);
+            u[j] = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
+          }
+          reinterpret_cast<uint4*>(a.cache[kind])[slot * kPieces + c] =
+              make_uint4(u[0] | (u[1] << 16), u[2] | (u[3] << 16), u[4] | (u[5] << 16), u[6] | (u[7] << 16));
+          if (c == 0) a.scale[kind][slot] = scale;
+        }
+      }
     }
   }
-  const int pieces = a.d / 8;  // 16 or 8 lanes hold a row
-  const int nq = a.q.ptr ? a.n_heads : 0;
-  const int total = (nq + 2 * a.n_kv) * pieces;
-  // whole warps take part in the shuffles: the bound is rounded up
-  for (int e = threadIdx.x; e < ((total + 31) & ~31); e += kThreads) {
-    const int c = e % pieces;
-    int h = e / pieces;
-    const bool live = e < total;
-    const gqa_rows* src = &a.q;
-    int kind = 0;
-    if (h >= nq) {
-      h -= nq;
-      kind = 1;
-      src = &a.k;
-      if (h >= a.n_kv) {
-        h -= a.n_kv;
-        kind = 2;
-        src = &a.v;
-      }
-    }
-    float x[8] = {};
-    if (live) {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(src->ptr) + i * src->row_stride + h * src->head_stride + 8 * c;
-      unpack8<kBf16>(*reinterpret_cast<const uint4*>(p), x);
-    }
-    const int at = 8 * c - (a.d - a.r);
-    if (kind < 2 && at >= 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float co = cs[at / 2 + j], si = sn[at / 2 + j], u = x[2 * j], w = x[2 * j + 1];
-        x[2 * j] = __fsub_rn(__fmul_rn(u, co), __fmul_rn(w, si));
-        x[2 * j + 1] = __fadd_rn(__fmul_rn(u, si), __fmul_rn(w, co));
-      }
-    }
-    const gqa_rows* dst = kind == 0 ? &a.q_out : &a.k_out;
-    const uint4 y = pack8<kBf16>(x);
-    if (live && kind < 2 && dst->ptr)
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(dst->ptr) + i * dst->row_stride + h * dst->head_stride +
-                                8 * c) = y;
-    const int64_t row = (page * a.n_kv + h) * a.page + slot;
-    if (!kFp8) {
-      if (live && kind > 0 && page >= 0)
-        reinterpret_cast<uint4*>(kind == 1 ? a.cache.k : a.cache.v)[row * pieces + c] = y;
-    } else {
-      float am = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) am = max_nan(am, fabsf(x[j]));
-      for (int o = pieces / 2; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
-      if (live && kind > 0 && page >= 0) {
-        const float scale = am == 0.f ? 1.f : __fdiv_rn(am, kE4M3Max);  // NaN in a row: a NaN scale
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j / 4] |= f32_to_e4m3_sat(__fdiv_rn(x[j], scale)) << (8 * (j % 4));
-        reinterpret_cast<uint2*>(kind == 1 ? a.cache.k : a.cache.v)[row * pieces + c] = make_uint2(w[0], w[1]);
-        if (c == 0) (kind == 1 ? a.cache.k_scale : a.cache.v_scale)[row] = scale;
-      }
-    }
+  pdl_trigger();
+}
+
+// The frequencies of a (theta, r), kept per host thread: 64 powers cost more
+// than the rest of the call.
+const double* turns_of(float theta, int r) {
+  thread_local float t_theta = 0.f;
+  thread_local int t_r = -1;
+  thread_local double t_turns[64];
+  if (t_theta != theta || t_r != r) {
+    for (int j = 0; j < 64; ++j)
+      t_turns[j] = 2 * j < r ? std::pow((double)theta, -2.0 * j / r) / 6.283185307179586476925 : 0.0;
+    t_theta = theta;
+    t_r = r;
   }
+  return t_turns;
 }
 
 }  // namespace
@@ -141,12 +241,27 @@ cudaError_t launch_gqa_append(const gqa_params& p, const gqa_rows& q, const gqa_
                               int64_t n_tokens, const int32_t* cu, const int32_t* pos0, const gqa_cache& cache,
                               const int32_t* table, int64_t table_cols, const gqa_rows& q_out, const gqa_rows& k_out,
                               int32_t* err, cudaStream_t st) {
-  const AppendArgs a{q, k, v, q_out, k_out, cache, cu, pos0, table, table_cols,
-                     p.B, p.n_heads, p.n_kv_heads, p.d, p.r, p.page, p.rope_theta, err};
+  // tokens per CTA: as many as fill the threads' first batch of loads, but no
+  // fewer CTAs than SMs
+  const int nq = q.ptr ? p.n_heads : 0, per_token = nq + 2 * p.n_kv_heads;
+  int tokens = kBatch * kThreads / (per_token * p.d / 16);
+  if (tokens > kMaxTokens) tokens = kMaxTokens;
+  const int64_t most = n_tokens / sm_count();
+  if (tokens > most) tokens = (int)most;
+  if (tokens < 1) tokens = 1;
+  int shift = 0;
+  while ((1 << shift) < p.page) ++shift;
+  AppendArgs a{{q, k, v}, {q_out, k_out}, {nullptr, cache.k, cache.v}, {nullptr, cache.k_scale, cache.v_scale},
+               cache.n_pages, cu, pos0, table, table_cols, (int)n_tokens, tokens, p.B, nq, p.n_kv_heads, p.r, p.page,
+               shift, tokens * per_token, per_token, (65536u + per_token - 1) / per_token, err, {}};
+  std::memcpy(a.turns, turns_of(p.rope_theta, p.r), sizeof(a.turns));
   const bool bf = p.act_fmt == CSA_ACT_BF16, f8 = p.kv_fmt == CSA_KV_FP8;
-  auto fn = bf ? (f8 ? gqa_append_kernel<true, true> : gqa_append_kernel<true, false>)
-               : (f8 ? gqa_append_kernel<false, true> : gqa_append_kernel<false, false>);
-  return launch_pdl(fn, dim3((unsigned)n_tokens), dim3(kThreads), 0, st, a);
+  auto pick = [&](auto k128, auto k64) { return p.d == 128 ? k128 : k64; };
+  auto fn = bf ? (f8 ? pick(gqa_append_kernel<true, true, 128>, gqa_append_kernel<true, true, 64>)
+                     : pick(gqa_append_kernel<true, false, 128>, gqa_append_kernel<true, false, 64>))
+               : (f8 ? pick(gqa_append_kernel<false, true, 128>, gqa_append_kernel<false, true, 64>)
+                     : pick(gqa_append_kernel<false, false, 128>, gqa_append_kernel<false, false, 64>));
+  return launch_pdl(fn, dim3((unsigned)((n_tokens + tokens - 1) / tokens)), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace csa
