@@ -397,7 +397,7 @@ csa_status csa_state_restore(const csa_params* params, const int32_t* pos, const
  * compressed layers above; sinks and sliding windows are those of
  * csa_sparse_attn.
  *
- *   B           sequences (1..2048)
+ *   B           sequences (1..1024)
  *   n_heads     query heads (1..128), a multiple of n_kv_heads; query head h
  *               reads KV head h / (n_heads / n_kv_heads)
  *   d           head dim, 64 or 128

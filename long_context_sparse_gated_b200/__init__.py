@@ -332,34 +332,37 @@ def make_gqa_cache(k, v, k_scale=None, v_scale=None) -> GqaCache:
 _NO_ROWS = GqaRows(None, 0, 0)
 
 
-def _gqa_types(params):
+def _gqa_types(params, x):
     """(torch dtype of act_fmt, current device) that every row tensor has to
-    match: kernels are launched on the current device."""
+    match: kernels are launched on the current device.  Device -1 if x is a
+    host tensor (refused by _on_device once shapes are checked)."""
     import torch
-    return torch.bfloat16 if params.act_fmt == ACT_BF16 else torch.float16, torch._C._cuda_getDevice()
+    return (torch.bfloat16 if params.act_fmt == ACT_BF16 else torch.float16,
+            torch._C._cuda_getDevice() if x.is_cuda else -1)
 
 
-def _rows(x, types, heads, d):
+def _on_device(types):
+    if types[1] < 0:
+        raise TypeError("libcsa takes CUDA tensors (device pointers); got a host array")
+
+
+def _rows(x, types, n, heads, d):
     """gqa_rows of a CUDA tensor [n, heads, d] of the activation type; only
     its last dim has to be contiguous."""
     dtype, device = types
     if x.get_device() != device:
         if not x.is_cuda:
-            raise TypeError("libcsa takes CUDA tensors (device pointers); got a host array")
+            _on_device((dtype, -1))
         raise ValueError(f"tensor on device {x.get_device()}, but device {device} is current")
     if x.dtype is not dtype:
         raise TypeError(f"act_fmt says {dtype}, got {x.dtype}")
-    n, h, last = x.shape
-    if h != heads or last != d:
-        raise ValueError(f"expected [n, {heads}, {d}], got {tuple(x.shape)}")
+    if x.shape != (n, heads, d):
+        raise ValueError(f"expected [{n}, {heads}, {d}], got {tuple(x.shape)}")
     sn, sh, sd = x.stride()
     if sd != 1:
         raise ValueError("the last dim of a row tensor has to be contiguous")
-    if n < 2:
-        sn = max(sn, d)  # the stride of a single row is never used
-    if h < 2:
-        sh = max(sh, d)
-    return GqaRows(x.data_ptr(), sn, sh)
+    # the stride of a single row or head is never used
+    return GqaRows(x.data_ptr(), sn if n > 1 else max(sn, d), sh if heads > 1 else max(sh, d))
 
 
 def gqa_cache_append(params, q, k, v, cu, pos0, cache, table, q_out=None, k_out=None, err=None, stream=None):
@@ -369,14 +372,14 @@ def gqa_cache_append(params, q, k, v, cu, pos0, cache, table, q_out=None, k_out=
     Turned queries (``q`` [n, n_heads, d], or None) go to ``q_out``, turned
     keys to ``k_out`` (both may be the inputs)."""
     n, d, hk, hq = k.shape[0], params.d, params.n_kv_heads, params.n_heads
-    for x in (v, q, q_out, k_out):
-        if x is not None and x.shape[0] != n:
-            raise ValueError("q, k, v, q_out and k_out have the same rows")
-    ty = _gqa_types(params) if k.is_cuda else (k.dtype, None)
-    st = lib().gqa_cache_append(
-        ctypes.byref(params), _NO_ROWS if q is None else _rows(q, ty, hq, d), _rows(k, ty, hk, d), _rows(v, ty, hk, d), n,
-        _ptr(cu), _ptr(pos0), cache, _ptr(table), table.shape[1], _NO_ROWS if q_out is None else _rows(q_out, ty, hq, d),
-        _NO_ROWS if k_out is None else _rows(k_out, ty, hk, d), _ptr(err), _stream(stream))
+    ty = _gqa_types(params, k)
+    rk, rv = _rows(k, ty, n, hk, d), _rows(v, ty, n, hk, d)
+    rq = _NO_ROWS if q is None else _rows(q, ty, n, hq, d)
+    rqo = _NO_ROWS if q_out is None else _rows(q_out, ty, n, hq, d)
+    rko = _NO_ROWS if k_out is None else _rows(k_out, ty, n, hk, d)
+    _on_device(ty)
+    st = lib().gqa_cache_append(ctypes.byref(params), rq, rk, rv, n, _ptr(cu), _ptr(pos0), cache, _ptr(table),
+                                table.shape[1], rqo, rko, _ptr(err), _stream(stream))
     if st:
         _check("gqa_cache_append", st)
 
@@ -389,13 +392,13 @@ def gqa_decode_attn(params, q, cache, table, lens, T, n_max, out, ws=None, sink=
     """The last T tokens of every sequence (``q``, ``out`` [B*T, n_heads, d])
     attend to the lens[b] <= n_max cached keys of their sequence; ``ws`` is a
     CUDA byte tensor of gqa_decode_attn_workspace_bytes(params, T, n_max)."""
-    if q.shape[0] != params.B * T or out.shape[0] != params.B * T:
-        raise ValueError("q and out have B * T rows")
-    ty = _gqa_types(params) if q.is_cuda else (q.dtype, None)
-    hq, d = params.n_heads, params.d
-    st = lib().gqa_decode_attn(
-        ctypes.byref(params), _rows(q, ty, hq, d), cache, _ptr(table), table.shape[1], _ptr(lens), T, n_max, _ptr(sink),
-        _rows(out, ty, hq, d), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(err), _stream(stream))
+    ty = _gqa_types(params, q)
+    n, hq, d = params.B * T, params.n_heads, params.d
+    rq, ro = _rows(q, ty, n, hq, d), _rows(out, ty, n, hq, d)
+    _on_device(ty)
+    st = lib().gqa_decode_attn(ctypes.byref(params), rq, cache, _ptr(table), table.shape[1], _ptr(lens), T, n_max,
+                               _ptr(sink), ro, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(err),
+                               _stream(stream))
     if st:
         _check("gqa_decode_attn", st)
 
@@ -405,12 +408,11 @@ def gqa_prompt_attn(params, q, k, v, cu_q, cu_k, out, sink=None, err=None, strea
     cu_q[b]..cu_q[b+1]-1 of ``q`` and ``out`` ([n_q, n_heads, d]), its keys
     and values rows cu_k[b]..cu_k[b+1]-1 of ``k`` and ``v`` ([n_k,
     n_kv_heads, d]); the last query sits at the last key."""
-    if out.shape[0] != q.shape[0] or v.shape[0] != k.shape[0]:
-        raise ValueError("q and out have the same rows, and k and v")
-    ty = _gqa_types(params) if q.is_cuda else (q.dtype, None)
-    hk, hq, d = params.n_kv_heads, params.n_heads, params.d
-    st = lib().gqa_prompt_attn(
-        ctypes.byref(params), _rows(q, ty, hq, d), _rows(k, ty, hk, d), _rows(v, ty, hk, d), q.shape[0], k.shape[0],
-        _ptr(cu_q), _ptr(cu_k), _ptr(sink), _rows(out, ty, hq, d), _ptr(err), _stream(stream))
+    ty = _gqa_types(params, q)
+    n, m, hk, hq, d = q.shape[0], k.shape[0], params.n_kv_heads, params.n_heads, params.d
+    rq, rk, rv, ro = _rows(q, ty, n, hq, d), _rows(k, ty, m, hk, d), _rows(v, ty, m, hk, d), _rows(out, ty, n, hq, d)
+    _on_device(ty)
+    st = lib().gqa_prompt_attn(ctypes.byref(params), rq, rk, rv, n, m, _ptr(cu_q), _ptr(cu_k), _ptr(sink), ro, _ptr(err),
+                               _stream(stream))
     if st:
         _check("gqa_prompt_attn", st)

@@ -306,7 +306,7 @@ static csa_status check_gqa(const gqa_params* p) {
   if (!p) return CSA_ERR_INVALID;
   if (p->B < 1 || p->n_heads < 1 || p->n_kv_heads < 1 || p->window < 0) return CSA_ERR_INVALID;
   if (p->n_heads % p->n_kv_heads) return CSA_ERR_INVALID;
-  if (p->B > 2048 || p->n_heads > 128) return CSA_ERR_UNSUPPORTED;
+  if (p->B > 1024 || p->n_heads > 128) return CSA_ERR_UNSUPPORTED;
   if (p->d != 64 && p->d != 128) return CSA_ERR_UNSUPPORTED;
   if (p->act_fmt != CSA_ACT_BF16 && p->act_fmt != CSA_ACT_F16) return CSA_ERR_UNSUPPORTED;
   if (!(p->softmax_scale > 0.f && p->softmax_scale <= 3.0e38f)) return CSA_ERR_INVALID;

@@ -8,36 +8,42 @@
 // bytes bound the call up to about a hundred rows per KV head.
 //
 // Work.  An item is one sequence's split of its keys, one KV head and up to
-// kNq of its T * G query rows.  Splits are a rule on the sequence's own tile
-// count (split_tiles), so a query's bits do not depend on its batch.  Every
-// warp works alone: worker w takes items w, w + workers, ... and leaves the
-// item's (m, l, O) in fp32 for gqa_join_kernel, or the result where the
-// sequence has one split.
+// kNq of its T * G query rows.  Splits are a rule on the sequence's own length
+// (split_blocks), so a query's bits do not depend on its batch.  A team of
+// four warps takes an item, its tiles in turn, and joins the four results in
+// shared memory; teams take items t, t + teams, ..., the largest splits first,
+// and leave an item's (m, l, O) in fp32 for gqa_join_kernel, or the result where
+// the sequence has one split.  (A warp needs some 0.9 us a tile when it is
+// alone, so one warp an item makes short contexts slow: 15.4 us for 777 keys;
+// all eight warps of a CTA an item costs long ones their join.)
 //
-//   tiles    16 keys and values, always inside one page.  A warp owns a ring
-//            of stages and refills each with TMA as soon as it has read it;
-//            the loading side runs ahead over item borders, so the stream of
-//            tiles never drains.  No barrier among warps, no producer: a
-//            first version joined eight warps' results per item in shared
-//            memory and spent twice the instructions on short splits.
-//   product  S^T[16 keys, rows] = K Q^T     (mma m16n8k16, K by ldmatrix)
-//            P^T = exp2(S^T - m), rounded to 16 bits, transposed in
-//            registers by movmatrix
-//            O^T[d, rows] += V^T P^T        (V by ldmatrix.trans)
-//            With the keys as M, 8 query rows fill an MMA (with rows as M
-//            the usual groups of 8 would waste half of it).
+//   tiles    16 keys and values, always inside one page, loaded by TMA.  A warp
+//            owns a ring of stages and refills each as soon as it has read it; the
+//            loading side runs ahead over item borders, so the stream of
+//            tiles never drains, and there is no producer to wait for.  With
+//            fewer items than teams, fewer teams have deeper rings.
+//   product  S^T[keys, rows] = K Q^T, P^T = exp2(S^T - m), O^T[d, rows] += V^T P^T
+//            by mma.sync.  With the keys as M, 8 query rows fill an MMA (with
+//            rows as M the usual groups of 8 would waste half of it).
 //
-// FP8 cache.  E4M3 codes become FP16 (of 2^-8 their value, exactly) in registers; the dims of a
-// 16-byte piece are dealt to MMA steps in an order that Q's fragments share,
-// so no shuffles are needed.  A query row is brought into FP16 by a power of
-// two of its own (largest magnitude in [2^14, 2^15); what is 2^29 below that
-// loses bits that do not show in fp32).  The value's scale s_j joins the
-// weight: w_j = exp2(z_j + log2 s_j - M) with M the running maximum of that
-// sum, so weights stay in (0, 1] whatever the scales are, and the
-// denominator sums exp2(z_j - M).  Scales are read as within 2^-90 .. 2^90.
+// 16-bit cache.  m16n8k16; K by ldmatrix, V by ldmatrix.trans, P^T rounded to
+// 16 bits and transposed in registers by movmatrix.
 //
-// Rounding.  Weights are rounded to the MMA's 16-bit type (relative 2^-9
-// for BF16, 2^-12 for FP16), sums and partial outputs are fp32.
+// FP8 cache.  E4M3 codes become FP16 in registers (m16n8k32 on 8-bit operands
+// is no way around it: here it compiles to conversions and m16n8k16), K's by
+// the conversion instruction, which goes through the 16-lane special-function
+// pipe, V's by moving bits, three or four ALU instructions for two codes.
+// One pipe alone takes 278 or 208 us for 24 sequences of up to 32K keys.  The
+// dims of a 16-byte piece are dealt to MMA steps in an order that Q's
+// fragments share, so no shuffles are needed.  A query row is brought into
+// FP16 by a power of two of its own (largest magnitude in [2^14, 2^15); what is
+// 2^29 below that loses bits that do not show in fp32).  The value's scale s_j
+// joins the weight: w_j = exp2(z_j + log2 s_j - M) with M the running maximum of
+// that sum, so weights stay in (0, 2^8] whatever the scales are, and the
+// denominator sums w_j / s_j.  Value scales are read as within 2^-90 .. 2^90.
+//
+// Rounding.  Weights are rounded to 16 bits (relative 2^-9 for a BF16 cache,
+// 2^-12 for FP16 and FP8 caches), sums and partial outputs are fp32.
 //
 // Masks.  Tiles of pages that are none are passed over.  Tiles that a row
 // does not see as a whole (the last ones, a window's first) take a path of
@@ -56,27 +62,29 @@ namespace {
 
 using namespace gqa;
 
-constexpr int kTile = 16;  // keys per stage
+constexpr int kTile = 16;   // keys per stage
+constexpr int kBlock = 32;  // keys: splits begin at multiples of it
+constexpr int kMaxStages = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;      // base-2 units
 constexpr float kMinLogScale = -90.f, kMaxLogScale = 90.f;
 
-// Tiles per split for a sequence of n tiles: about 32 splits of 8 to 32 tiles
-// (128 to 512 keys).
-constexpr int kMinSplit = 8, kMaxSplit = 32, kSplits = 32;
-__host__ __device__ inline int split_tiles(int n) {
+// Blocks per split for a sequence of n blocks: about 32 splits of 4 to 16
+// blocks (128 to 512 keys).
+constexpr int kMinSplit = 4, kMaxSplit = 16, kSplits = 32;
+__host__ __device__ inline int split_blocks(int n) {
   int c = kMinSplit;
   while (c < kMaxSplit && c * kSplits < n) c *= 2;
   return c;
 }
 __host__ __device__ inline int n_splits(int n) {
-  const int c = split_tiles(n);
+  const int c = split_blocks(n);
   return n <= c ? 1 : (n + c - 1) / c;  // a sequence without keys has one empty split
 }
-// The most splits that any sequence of up to n tiles has.
+// The most splits that any sequence of up to n blocks has.
 inline int most_splits(int n) {
   int most = n_splits(n);
-  for (int c = kMinSplit; c < kMaxSplit; c *= 2)  // the longest sequence cut into c tiles
+  for (int c = kMinSplit; c < kMaxSplit; c *= 2)  // the longest sequence cut into c blocks
     if (c * kSplits < n && most < kSplits) most = kSplits;
   return most;
 }
@@ -97,17 +105,17 @@ struct DecodeArgs {
   int32_t* err;
 };
 
-// Keys [lo, hi) that some query of the sequence sees, and the tiles that
-// hold them.
+// The keys [lo, len) that some query of the sequence sees, and the n blocks
+// from block b0 on that hold them.
 struct Span {
-  int len, lo, t0, n;
+  int len, lo, b0, n;
 };
 __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b) {
   Span s;
   s.len = max(0, min(a.lens[b], a.n_max));
   s.lo = a.window > 0 ? max(0, s.len - a.T - a.window + 1) : 0;
-  s.t0 = s.lo / kTile;
-  s.n = s.len > s.lo ? (s.len + kTile - 1) / kTile - s.t0 : 0;
+  s.b0 = s.lo / kBlock;
+  s.n = s.len > s.lo ? (s.len + kBlock - 1) / kBlock - s.b0 : 0;
   return s;
 }
 
@@ -145,24 +153,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// E4M3 codes in bytes 1 and 3 (bytes 0 and 2) -> two FP16 of 2^-8 their
-// value: sign, four exponent and three mantissa bits move to FP16's places
-// (its exponent bias is 8 larger), subnormals included.  Three or four ALU
-// instructions for two codes; the conversion instruction goes through the
-// 16-lane special-function pipe, which 128 codes a lane and 16 keys fill.
-// `top` gathers the largest magnitudes, which tell whether a NaN code was
-// among them (they come out as +-480 here).
-__device__ __forceinline__ uint32_t codes13_to_f16x2(uint32_t v, uint32_t& top) {
-  const uint32_t mag = (v >> 1) & 0x3F803F80u;
-  top = __vmaxu2(top, mag);
-  return (v & 0x80008000u) | mag;
-}
-__device__ __forceinline__ uint32_t codes02_to_f16x2(uint32_t v, uint32_t& top) { return codes13_to_f16x2(v << 8, top); }
-__device__ __forceinline__ bool has_nan_code(uint32_t top) {
-  return (top & 0xFFFFu) == 0x3F80u || (top >> 16) == 0x3F80u;
-}
-constexpr float kCodeExp = 8.f, kCodeFactor = 256.f;
-
 __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -180,7 +170,7 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return v;
 }
 
-// K or V of a tile: 16 rows of one page and head, the 64-dim halves of a
+// A box of K or V: 16 rows of one page and head, the 64-dim halves of a
 // 16-bit row one after the other.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
   asm volatile(
@@ -189,6 +179,25 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(sm100::smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
+// Two E4M3 codes (low 16 bits) -> two FP16.
+__device__ __forceinline__ uint32_t cvt_codes(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+// E4M3 codes in bytes 1 and 3 (bytes 0 and 2) -> two FP16 of 2^-8 their
+// value: sign, four exponent and three mantissa bits move to FP16's places
+// (its exponent bias is 8 larger), subnormals included.  `mag` is their
+// magnitude: the NaN codes come out as 0x3F80 (+-480 / 2^8).
+__device__ __forceinline__ uint32_t move_codes13(uint32_t v, uint32_t& mag) {
+  mag = (v >> 1) & 0x3F803F80u;
+  return (v & 0x80008000u) | mag;
+}
+__device__ __forceinline__ uint32_t move_codes02(uint32_t v, uint32_t& mag) { return move_codes13(v << 8, mag); }
+__device__ __forceinline__ bool has_nan_code(uint32_t top) {
+  return (top & 0xFFFFu) == 0x3F80u || (top >> 16) == 0x3F80u;
+}
+constexpr float kCodeExp = 8.f;  // of the moved codes
+
 // Halves of a register that are infinities or NaN, as a mask over them.
 template <bool kBf16>
 __device__ __forceinline__ uint32_t odd_halves(uint32_t v) {
@@ -196,22 +205,28 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t v) {
   return ((v & e) == e ? 0xFFFFu : 0u) | ((v & (e << 16)) == (e << 16) ? 0xFFFF0000u : 0u);
 }
 
+constexpr int kTeam = 4;  // warps
+constexpr int kMaxB = 1024;
+
 template <bool kFp8, int kD, int kNq>
 struct Layout {
-  // 12 warps of up to 168 registers hold 8 query rows each, 8 warps 16 rows
-  static constexpr int kWarps = kNq == 8 ? 12 : 8;
+  // three teams of up to 168 registers a thread, or two of up to 255
+  static constexpr int kTeams = kNq == 8 ? 3 : 2, kWarps = kTeam * kTeams;
   static constexpr int kRowBytes = kFp8 ? kD : 2 * kD;
-  static constexpr int kOperand = kTile * kRowBytes;          // K or V of a tile
-  static constexpr int kScales = kFp8 ? 2 * kTile * 4 : 0;    // its scales, K then V
+  static constexpr int kOperand = kTile * kRowBytes;       // K or V of a tile
   static constexpr int kStage = 2 * kOperand;
-  static constexpr int kStages = 196608 / kWarps / kStage;    // per warp: about 192 KB in flight on an SM
-  static constexpr size_t kSmem = 1024 + (size_t)kWarps * kStages * (kStage + kScales);
+  static constexpr int kScales = kFp8 ? 2 * kTile * 4 : 0;  // its scales, K then V
+  static constexpr int kSlots = kFp8 ? (kD == 128 ? 36 : 72) : (kD == 128 ? 24 : 48);  // stages of all warps
+  static constexpr int kJoin = 2 * kD * 8 * 4;              // a team's buffer: two warps' 8 rows
+  static constexpr size_t kSmem = 1024 + (size_t)kSlots * (kStage + kScales) + kTeams * kJoin;
+  static_assert(kSmem + 8704 <= 232448, "shared memory of a CTA");
 };
 
-// Where a worker stands: its item, and the tile in it.
-struct Cursor {
-  int item, b, kvh, split, chunk;  // chunk: which kNq of the query rows
-  int t, t_end;                    // tiles of 16 keys from the sequence's start
+// An item and the stretch of keys in it that has to be read.
+struct Item {
+  int at;                  // in the order of sequences
+  int b, kvh, split, chunk;  // chunk: which kNq of the query rows
+  int t, t_end;            // this warp's tiles: t, t + kTeam, ... of the sequence's
   Span s;
 };
 
@@ -220,88 +235,111 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                       const DecodeArgs a) {
   using L = Layout<kFp8, kD, kNq>;
-  constexpr bool kMmaBf16 = kBf16 && !kFp8;  // FP8 codes are exact in FP16
   constexpr int kNt = kNq / 8;
+  constexpr bool kMmaBf16 = kBf16 && !kFp8;
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t full_bar[L::kWarps][L::kStages];
-  __shared__ int first_item[2049];  // items before sequence b
+  __shared__ uint64_t full_bar[L::kSlots];
+  __shared__ int first_item[kMaxB + 1];  // items before the i-th sequence of the order
+  __shared__ uint16_t order[kMaxB];      // sequences, those with the largest splits first
+  __shared__ float red_m[L::kTeams][2][kTeam][kNq], red_l[L::kTeams][2][kTeam][kNq];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* all = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* ring = all + warp * L::kStages * L::kStage;
-  float* scales = reinterpret_cast<float*>(all + L::kWarps * L::kStages * L::kStage + warp * L::kStages * L::kScales);
-  uint64_t* full = full_bar[warp];
 
-  if (lane == 0) {
-    for (int s = 0; s < L::kStages; ++s) sm100::mbar_init(&full[s], 1);
-    sm100::fence_mbar_init();
-    if (warp == 0) {
-      abort_flag = 0;
-      sm100::prefetch_tmap(&map_k);
-      sm100::prefetch_tmap(&map_v);
-    }
+  for (int s = threadIdx.x; s < L::kSlots; s += blockDim.x) sm100::mbar_init(&full_bar[s], 1);
+  sm100::fence_mbar_init();
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    sm100::prefetch_tmap(&map_k);
+    sm100::prefetch_tmap(&map_v);
   }
   pdl_wait();
+  pdl_trigger();  // gqa_join_kernel may take its place; it waits for this kernel's end
   const int G = a.n_heads / a.n_kv, rows = a.T * G;
   const int chunks = (rows + kNq - 1) / kNq;
+  // ---- the order of the sequences and their items.  (The ring's memory holds
+  // the counts until the first loads.)
+  int* counts = reinterpret_cast<int*>(all);
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+    const int n = span_of(a, b).n;
+    counts[b] = n_splits(n) * 32 + split_blocks(n);
+    if (blockIdx.x == 0 && a.lens[b] > a.n_max) raise_err(a.err, CSA_DEV_ERR_RANGE);
+  }
+  __syncthreads();
   if (warp == 0) {
-    int base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      int n = 0;
-      if (b0 + lane < a.B) {
-        n = n_splits(span_of(a, b0 + lane).n) * a.n_kv * chunks;
-        if (blockIdx.x == 0 && a.lens[b0 + lane] > a.n_max) raise_err(a.err, CSA_DEV_ERR_RANGE);
-      }
-      int x = n;
+    int items = 0, place = 0;
+    for (int c = kMaxSplit; c >= kMinSplit; c /= 2)
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int x = b0 + lane < a.B ? counts[b0 + lane] : 0;
+        const bool mine = (x & 31) == c;
+        const unsigned who = __ballot_sync(0xffffffffu, mine);
+        if (!who) continue;
+        const int n = mine ? (x >> 5) * a.n_kv * chunks : 0;
+        int sum = n;
 #pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        for (int o = 1; o < 32; o *= 2) {
+          const int y = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += y;
+        }
+        if (mine) {
+          const int i = place + __popc(who & ((1u << lane) - 1));
+          first_item[i] = items + sum - n;
+          order[i] = (uint16_t)(b0 + lane);
+        }
+        items += __shfl_sync(0xffffffffu, sum, 31);
+        place += __popc(who);
       }
-      if (b0 + lane < a.B) first_item[b0 + lane] = base + x - n;
-      base += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) first_item[a.B] = base;
+    if (lane == 0) first_item[a.B] = items;
+    sm100::fence_proxy_async_smem();  // the counts' place is loaded over
   }
   __syncthreads();
   const int total = first_item[a.B];
-  // workers are numbered across the SMs first
-  const int worker = warp * gridDim.x + blockIdx.x, workers = L::kWarps * gridDim.x;
+  // teams with work, numbered across the SMs first
+  const int team = warp / kTeam, w4 = warp % kTeam;
+  const int teams = max(1, min(L::kTeams, (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x));
+  const int item0 = team * gridDim.x + blockIdx.x, step = L::kTeams * gridDim.x;
+  if (team >= teams) return;
+  // ---- this warp's ring
+  const int n_st = min(kMaxStages, L::kSlots / (kTeam * teams));
+  uint8_t* ring = all + warp * n_st * L::kStage;
+  float* scales = reinterpret_cast<float*>(all + L::kSlots * L::kStage + warp * n_st * L::kScales);
+  float4* join = reinterpret_cast<float4*>(all + L::kSlots * (L::kStage + L::kScales) + team * L::kJoin);
+  uint64_t* full = full_bar + warp * n_st;
   volatile int* abort = &abort_flag;
 
-  // Enters the cursor's item (or runs past the end).
-  auto enter = [&](Cursor& c) {
-    if (c.item >= total) return;
-    while (c.item >= first_item[c.b + 1]) ++c.b;
-    const int in_b = c.item - first_item[c.b], x = in_b / chunks;
+  auto enter = [&](Item& c, int item) {
+    while (item >= first_item[c.at + 1]) ++c.at;
+    c.b = order[c.at];
+    const int in_b = item - first_item[c.at], x = in_b / chunks;
     c.chunk = in_b - x * chunks;
     c.split = x / a.n_kv;
     c.kvh = x - c.split * a.n_kv;
     c.s = span_of(a, c.b);
-    const int n = split_tiles(c.s.n);
-    c.t = c.s.t0 + c.split * n;
-    c.t_end = min(c.t + n, c.s.t0 + c.s.n);
+    const int n = split_blocks(c.s.n), b0 = c.s.b0 + c.split * n;
+    c.t = max(b0 * kBlock, c.s.lo) / kTile + w4;
+    c.t_end = c.s.n == 0 ? 0 : (min((b0 + n) * kBlock, c.s.len) + kTile - 1) / kTile;
   };
 
-  // ---- loading side: page ids 32 at a time, then one tile per free stage
-  Cursor ld;
-  ld.item = worker;
-  ld.b = 0;
-  enter(ld);
-  int ids = -1, group = -1;  // this lane's page id of 32-page group `group` of the item's sequence
-  uint32_t issued = 0;       // tiles given a stage so far
-  uint32_t none = 0;         // stages whose tile belongs to no page (nothing is loaded)
-  // The next tile of the loading side goes to stage issued % kStages; false
-  // at the end of the work.
-  auto load_next = [&]() {
-    while (ld.item < total) {
+  // ---- loading side: page ids 32 at a time, then tiles as long as stages are
+  // free
+  Item ld;
+  ld.at = 0;
+  ld.t = ld.t_end = 0;
+  int next = item0;           // the next item to load
+  uint32_t issued = 0, done = 0;
+  int st_ld = 0;              // issued % n_st
+  int ids = -1, group = -1;   // this lane's page id of 32-page group `group`
+  uint32_t none = 0;          // stages whose tile belongs to no page (nothing is loaded)
+  auto fill = [&]() {
+    while (issued - done < (uint32_t)n_st) {
       if (ld.t >= ld.t_end) {
-        ld.item += workers;
-        enter(ld);
+        if (next >= total) return;
+        enter(ld, next);
+        next += step;
         group = -1;
         continue;
       }
-      const int p = (ld.t * kTile) >> a.page_shift;
+      const int key = ld.t * kTile, p = key >> a.page_shift;
       if ((p >> 5) != group) {
         group = p >> 5;
         const int mine = 32 * group + lane;
@@ -314,44 +352,47 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
         }
       }
       const int id = __shfl_sync(0xffffffffu, ids, p & 31);
-      const int st = issued % L::kStages;
+      const int st = st_ld;
       none = id >= 0 ? none & ~(1u << st) : none | (1u << st);
       if (lane == 0) {
         if (id >= 0) {
           sm100::mbar_arrive_expect_tx(&full[st], L::kStage + L::kScales);
           uint8_t* dst = ring + st * L::kStage;
-          const int slot = (ld.t * kTile) & (a.page - 1), head_page = id * a.n_kv + ld.kvh;
+          const int slot = key & (a.page - 1), head_page = id * a.n_kv + ld.kvh;
           tma_load_4d(dst, &map_k, &full[st], 0, slot, 0, head_page);
           tma_load_4d(dst + L::kOperand, &map_v, &full[st], 0, slot, 0, head_page);
           if (kFp8) {
             const int64_t at = (int64_t)head_page * a.page + slot;
-            sm100::bulk_load(scales + st * 2 * kTile, a.k_scale + at, kTile * 4, &full[st]);
-            sm100::bulk_load(scales + st * 2 * kTile + kTile, a.v_scale + at, kTile * 4, &full[st]);
+            float* sc = scales + st * 2 * kTile;
+            sm100::bulk_load(sc, a.k_scale + at, kTile * 4, &full[st]);
+            sm100::bulk_load(sc + kTile, a.v_scale + at, kTile * 4, &full[st]);
           }
         } else {
           sm100::mbar_arrive(&full[st]);
         }
       }
-      ++ld.t;
+      ld.t += kTeam;
       ++issued;
-      return;
+      if (++st_ld == n_st) st_ld = 0;
     }
   };
-  for (int i = 0; i < L::kStages; ++i) load_next();
+  fill();
 
   // ---- computing side
   const int g = lane >> 2, q4 = lane & 3;
-  uint32_t done = 0;
   bool lost = false;
-  Cursor c;
-  c.b = 0;
-  for (c.item = worker; c.item < total && !lost; c.item += workers) {
-    enter(c);
-    const bool single = c.s.n <= split_tiles(c.s.n);
+  int st = 0;            // done % n_st
+  uint32_t phase = 0;    // of the stage
+  int par = 0;
+  Item c;
+  c.at = 0;
+  for (int item = item0; item < total; item += step, par ^= 1) {
+    enter(c, item);
+    const bool single = c.s.n <= split_blocks(c.s.n);
 
     // query fragments: B operand, column g of n-tile nt is query row
     // chunk * kNq + 8 nt + g = tau * G + head
-    uint32_t qf[kNt][kD / 16][2];
+    uint32_t qf[kNt][kD / 8];
     float qs[kNt][2];  // logit factor of columns 2 q4, 2 q4 + 1
     int tq[kNt][2];    // their positions (INT_MIN: no row)
 #pragma unroll
@@ -366,7 +407,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
         for (int kk = 0; kk < kD / 16; ++kk)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            qf[nt][kk][e] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 * e + 2 * q4) : 0u;
+            qf[nt][2 * kk + e] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 * e + 2 * q4) : 0u;
         qs[nt][0] = qs[nt][1] = a.scale;
       } else {
         // this lane's dims: kD/4 consecutive ones from kD/4 * q4 on
@@ -392,15 +433,14 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] *= down;
           const uint4 u = pack8<false>(f);
-          // dims 0, 2 and 1, 3 of each four, as the codes of a word come out
-          qf[nt][2 * i][0] = __byte_perm(u.x, u.y, 0x5410);
-          qf[nt][2 * i][1] = __byte_perm(u.x, u.y, 0x7632);
-          qf[nt][2 * i + 1][0] = __byte_perm(u.z, u.w, 0x5410);
-          qf[nt][2 * i + 1][1] = __byte_perm(u.z, u.w, 0x7632);
+          qf[nt][4 * i] = u.x;
+          qf[nt][4 * i + 1] = u.y;
+          qf[nt][4 * i + 2] = u.z;
+          qf[nt][4 * i + 3] = u.w;
         }
         // column c's factor sits in lanes 4 c .. 4 c + 3
-        qs[nt][0] = kCodeFactor * a.scale * __shfl_sync(0xffffffffu, up, 8 * q4);
-        qs[nt][1] = kCodeFactor * a.scale * __shfl_sync(0xffffffffu, up, 8 * q4 + 4);
+        qs[nt][0] = a.scale * __shfl_sync(0xffffffffu, up, 8 * q4);
+        qs[nt][1] = a.scale * __shfl_sync(0xffffffffu, up, 8 * q4 + 4);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -420,24 +460,26 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
         for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
     }
 
-    for (; c.t < c.t_end; ++c.t, ++done) {
-      const int st = done % L::kStages;
-      lost = __any_sync(0xffffffffu, !sm100::mbar_wait(&full[st], (done / L::kStages) & 1, abort));
+    for (; c.t < c.t_end && !lost; c.t += kTeam) {
+      lost = __any_sync(0xffffffffu, !sm100::mbar_wait(&full[st], phase, abort));
       if (lost) break;
       if (!((none >> st) & 1)) {
         const int key0 = c.t * kTile;
         const uint32_t sk = sm100::smem_u32(ring + st * L::kStage), sv = sk + L::kOperand;
-        // not seen by every row: keys after the first query, before the last query's window
+        // not seen by every row: keys after the first query, before the last
+        // query's window
         const bool edge = key0 + kTile - 1 > c.s.len - a.T || (a.window > 0 && key0 < c.s.len - a.window);
-        auto seen = [&](int key, int tcol) { return key <= tcol && (a.window == 0 || key > tcol - a.window); };
+        auto seen = [&](int k, int tcol) {  // the tile's k-th key
+          const int key = key0 + k;
+          return key <= tcol && (a.window == 0 || key > tcol - a.window);
+        };
 
-        // S^T = K Q^T, in two chains of MMAs
+        // S^T = K Q^T (keys g, g + 8), in two chains of MMAs
         float z[kNt][4], z2[kNt][4];
 #pragma unroll
         for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[nt][e] = z2[nt][e] = 0.f;
-        uint32_t top_k[2] = {0, 0};  // largest magnitudes of the codes of keys g, g + 8
         if (!kFp8) {
           const int r = lane & 15;
 #pragma unroll
@@ -446,7 +488,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
             const int ch = 2 * (kk & 3) + (lane >> 4);
             ldsm4(sk + (kk >> 2) * kTile * 128 + r * 128 + ((ch ^ (r & 7)) << 4), af);
 #pragma unroll
-            for (int nt = 0; nt < kNt; ++nt) mma16816<kMmaBf16>((kk & 1) ? z2[nt] : z[nt], af, qf[nt][kk][0], qf[nt][kk][1]);
+            for (int nt = 0; nt < kNt; ++nt) mma16816<kMmaBf16>((kk & 1) ? z2[nt] : z[nt], af, qf[nt][2 * kk], qf[nt][2 * kk + 1]);
           }
         } else {
           // 16 codes of keys g and g + 8 at a time: four MMA steps, whose dims
@@ -462,16 +504,15 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
             const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
             for (int sp = 0; sp < 4; ++sp) {
-              const uint32_t af[4] = {codes02_to_f16x2(w0[sp], top_k[0]), codes02_to_f16x2(w1[sp], top_k[1]),
-                                      codes13_to_f16x2(w0[sp], top_k[0]), codes13_to_f16x2(w1[sp], top_k[1])};
+              const uint32_t af[4] = {cvt_codes(w0[sp]), cvt_codes(w1[sp]), cvt_codes(w0[sp] >> 16), cvt_codes(w1[sp] >> 16)};
 #pragma unroll
               for (int nt = 0; nt < kNt; ++nt)
-                mma16816<false>((sp & 1) ? z2[nt] : z[nt], af, qf[nt][4 * i + sp][0], qf[nt][4 * i + sp][1]);
+                mma16816<false>((sp & 1) ? z2[nt] : z[nt], af, qf[nt][8 * i + 2 * sp], qf[nt][8 * i + 2 * sp + 1]);
             }
           }
         }
-        // of keys g, g + 8: K scale, log2 of the V scale (codes come as 2^-8 of
-        // their value) and 2^ of its negative
+        // of keys g, g + 8: K scale, log2 of the V scale (V's codes come as 2^-8
+        // of their value) and 2^ of its negative
         float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f}, rv[2] = {1.f, 1.f};
         if (kFp8) {
           const float* sc = scales + st * 2 * kTile + g;
@@ -482,38 +523,29 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
             lv[e] = x != x ? x : fminf(fmaxf(lg2(x), kMinLogScale), kMaxLogScale) + kCodeExp;
             rv[e] = ex2(-lv[e]);
           }
-          const bool nan_k = has_nan_code(top_k[0]) || has_nan_code(top_k[1]);
-          if (__any_sync(0xffffffffu, nan_k)) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              int bad = has_nan_code(top_k[e]);
-              bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-              bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
-              if (bad) ks[e] = __int_as_float(0x7FC00000);
-            }
-          }
         }
-        float u[kNt][4];  // base-2 logit plus the value's log-scale; masked ones -inf
+        // base-2 logit plus the value's log-scale; masked ones -inf
         bool over = false;
 #pragma unroll
         for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float zz = (z[nt][e] + z2[nt][e]) * (kFp8 ? qs[nt][e & 1] * ks[e >> 1] : qs[nt][e & 1]);
-            u[nt][e] = kFp8 ? zz + lv[e >> 1] : zz;
-            if (edge && !seen(key0 + g + 8 * (e >> 1), tq[nt][e & 1])) u[nt][e] = -INFINITY;
-            over |= u[nt][e] > m[nt][e & 1] + kLazy;
+            float& u = z[nt][e];
+            u += z2[nt][e];
+            u = kFp8 ? fmaf(u, qs[nt][e & 1] * ks[e >> 1], lv[e >> 1]) : u * qs[nt][e & 1];
+            if (edge && !seen(g + 8 * (e >> 1), tq[nt][e & 1])) u = -INFINITY;
+            over |= u > m[nt][e & 1] + kLazy;
           }
         // The running maxima move only when a logit exceeds them by kLazy
         // (weights then stay below 2^kLazy): mostly one vote instead of
-        // shuffles over the 16 keys and a pass over O.
+        // shuffles over the keys and a pass over O.
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int nt = 0; nt < kNt; ++nt) {
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float v = fmaxf(u[nt][e], u[nt][e + 2]);
+              float v = fmaxf(z[nt][e], z[nt][e + 2]);
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
@@ -530,23 +562,23 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
               for (int e = 0; e < 4; ++e) o[mt][nt][e] *= alpha[e & 1];
           }
         }
+        // weights, transposed: B operand of the second product
         uint32_t pf[kNt][2];
 #pragma unroll
         for (int nt = 0; nt < kNt; ++nt) {
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float mr = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-            p[e] = ex2(u[nt][e] - mr);
+            const float u = z[nt][e];
+            p[e] = ex2(u - (m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1]));
             if (!kFp8) l[nt][e & 1] += p[e];
-            else if (!edge || u[nt][e] != -INFINITY) l[nt][e & 1] = fmaf(p[e], rv[e >> 1], l[nt][e & 1]);
+            else if (!edge || u != -INFINITY) l[nt][e & 1] = fmaf(p[e], rv[e >> 1], l[nt][e & 1]);
           }
           pf[nt][0] = transpose8x8(pack2<kMmaBf16>(p[0], p[1]));
           pf[nt][1] = transpose8x8(pack2<kMmaBf16>(p[2], p[3]));
         }
 
-        // O^T += V^T P^T.  Rows g, g + 8 of m-tile mt are dims dim_of(mt, 0),
-        // dim_of(mt, 1).
+        // O^T += V^T P^T
         bool odd = false;  // values that are not finite, taken out
         if (!kFp8) {
           const int i = lane >> 3, r = (lane & 7) + 8 * (i >> 1);
@@ -567,8 +599,9 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
             for (int nt = 0; nt < kNt; ++nt) mma16816<kMmaBf16>(o[mt][nt], af, pf[nt][0], pf[nt][1]);
           }
         } else {
-          // kD/8 codes of keys 2 q4, 2 q4 + 1, + 8, + 9 from dim kD/8 * g on
-          uint32_t w[4][kD / 32], top_v = 0;
+          // kD/8 codes of keys 2 q4, 2 q4 + 1, + 8, + 9 from dim kD/8 * g on: rows
+          // g and g + 8 of m-tile mt are dims 2 mt and 2 mt + 1 of that piece
+          uint32_t w[4][kD / 32], top = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = 2 * q4 + (e & 1) + 8 * (e >> 1);
@@ -586,15 +619,16 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
           }
 #pragma unroll
           for (int mt = 0; mt < kD / 16; ++mt) {
-            // dims 2 mt, 2 mt + 1 of the piece, of two keys each
             const uint32_t sel = (mt & 1) ? 0x7632u : 0x5410u;
             const uint32_t lo = __byte_perm(w[0][mt / 2], w[1][mt / 2], sel), hi = __byte_perm(w[2][mt / 2], w[3][mt / 2], sel);
-            const uint32_t af[4] = {codes02_to_f16x2(lo, top_v), codes13_to_f16x2(lo, top_v), codes02_to_f16x2(hi, top_v),
-                                    codes13_to_f16x2(hi, top_v)};
+            uint32_t mag[4];
+            const uint32_t af[4] = {move_codes02(lo, mag[0]), move_codes13(lo, mag[1]), move_codes02(hi, mag[2]),
+                                    move_codes13(hi, mag[3])};
+            top = __vimax3_u16x2(__vimax3_u16x2(top, mag[0], mag[1]), mag[2], mag[3]);
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt) mma16816<false>(o[mt][nt], af, pf[nt][0], pf[nt][1]);
           }
-          odd = has_nan_code(top_v);
+          odd = has_nan_code(top);
         }
         if (__any_sync(0xffffffffu, odd)) {
           // give each value that is not finite to the rows that see it
@@ -618,21 +652,25 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
                   for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                      if (seen(key0 + k, tq[nt][e])) o[mt][nt][2 * e2 + e] += v;
+                      if (seen(k, tq[nt][e])) o[mt][nt][2 * e2 + e] += v;
                 }
               }
             }
         }
       }
       __syncwarp();  // every lane has read the stage
-      load_next();
+      ++done;
+      if (++st == n_st) {
+        st = 0;
+        phase ^= 1;
+      }
+      fill();
     }
-    if (lost) break;
 
-    // ---- the item's result: sums over the keys of a column sit in its 8 lanes
+    // ---- the team's result (after a lost wait the barriers are still met):
+    // sums over the keys of a column sit in its 8 lanes
 #pragma unroll
-    for (int nt = 0; nt < kNt; ++nt) {
-      float f[2];
+    for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float v = l[nt][e];
@@ -640,9 +678,63 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
         v += __shfl_xor_sync(0xffffffffu, v, 8);
         v += __shfl_xor_sync(0xffffffffu, v, 16);
         l[nt][e] = v;
+        if (g == 0) {
+          red_m[team][par][w4][8 * nt + 2 * q4 + e] = m[nt][e];
+          red_l[team][par][w4][8 * nt + 2 * q4 + e] = v;
+        }
+      }
+    sm100::named_bar_sync(1 + team, 32 * kTeam);
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt) {
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = 8 * nt + 2 * q4 + e;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kTeam; ++w) top = fmaxf(top, red_m[team][par][w][col]);
+        const float mr = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int w = 0; w < kTeam; ++w) sum = fmaf(red_l[team][par][w][col], ex2(red_m[team][par][w][col] - mr), sum);
+        f[e] = ex2(m[nt][e] - mr);
+        m[nt][e] = top;
+        l[nt][e] = sum;
+      }
+#pragma unroll
+      for (int mt = 0; mt < kD / 16; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f[e & 1];
+      // warps 2 and 3 to 0 and 1, then 1 to 0: a lane's registers go to the
+      // same lane
+      if (nt > 0) sm100::named_bar_sync(1 + team, 32 * kTeam);  // the buffer is read
+      auto give = [&](int buf) {
+#pragma unroll
+        for (int mt = 0; mt < kD / 16; ++mt)
+          join[(buf * kD / 16 + mt) * 32 + lane] = make_float4(o[mt][nt][0], o[mt][nt][1], o[mt][nt][2], o[mt][nt][3]);
+      };
+      auto take = [&](int buf) {
+#pragma unroll
+        for (int mt = 0; mt < kD / 16; ++mt) {
+          const float4 v = join[(buf * kD / 16 + mt) * 32 + lane];
+          o[mt][nt][0] += v.x;
+          o[mt][nt][1] += v.y;
+          o[mt][nt][2] += v.z;
+          o[mt][nt][3] += v.w;
+        }
+      };
+      if (w4 >= 2) give(w4 & 1);
+      sm100::named_bar_sync(1 + team, 32 * kTeam);
+      if (w4 < 2) take(w4);
+      if (w4 == 1) give(1);
+      sm100::named_bar_sync(1 + team, 32 * kTeam);
+      if (w4 != 0) continue;
+      take(1);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
         f[e] = 1.f;
         if (single) {
           const int r = c.chunk * kNq + 8 * nt + 2 * q4 + e;
+          float v = l[nt][e];
           if (a.sink && r < rows && m[nt][e] != -INFINITY) v += ex2(a.sink[c.kvh * G + r % G] * kLog2e - m[nt][e]);
           f[e] = v != 0.f ? 1.f / v : 0.f;
         }
@@ -700,70 +792,96 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
     }
   }
   if (lost) {
-    // a wait gave up: copies in flight land before the CTA goes
+    // a wait gave up: copies in flight land before the warp goes
     for (; done < issued; ++done) {
       const uint64_t t0 = sm100::globaltimer();
-      while (!sm100::mbar_try_wait(&full[done % L::kStages], (done / L::kStages) & 1) && sm100::globaltimer() - t0 < sm100::kWaitNs) {
+      while (!sm100::mbar_try_wait(&full[st], phase) && sm100::globaltimer() - t0 < sm100::kWaitNs) {
+      }
+      if (++st == n_st) {
+        st = 0;
+        phase ^= 1;
       }
     }
     if (lane == 0) raise_err(a.err, CSA_DEV_ERR_TIMEOUT);
   }
-  pdl_trigger();
 }
 
 // Joins the splits of one (query row, head): M = max m_s, o = sum_s
 // exp2(m_s - M) O_s / (exp2(sink - M) + sum_s exp2(m_s - M) l_s).  One CTA
-// per row; warp w takes splits w, w + 8, ... in order and the warps are added
-// in order.
+// per row.  Warp w takes splits w, w + 8, ..., 32 at a time: a lane reads one
+// split's (m, l) while the outputs are already on their way; the warps'
+// results are then added in order.
 template <bool kBf16, int kD>
 __global__ void __launch_bounds__(256) gqa_join_kernel(const DecodeArgs a) {
+  constexpr int kV = kD / 32;
   __shared__ float red[8][kD];
   __shared__ float red_l[8], red_m[8];
-  pdl_wait();
   const int row = blockIdx.x, h = blockIdx.y, b = row / a.T, tau = row % a.T;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (lens was complete before gqa_decode_kernel let this kernel begin)
   const int n = n_splits(span_of(a, b).n);
+  const float sink = a.sink ? a.sink[h] * kLog2e : -INFINITY;
+  pdl_wait();
   if (n == 1) return;  // finished by gqa_decode_kernel
   const int64_t stride = (int64_t)a.T * a.n_heads;
   const int64_t slot = (int64_t)b * a.max_splits * stride + tau * a.n_heads + h;
-  float M = -INFINITY;
-  for (int s = threadIdx.x; s < n; s += 256) M = fmaxf(M, a.part_ml[slot + s * stride].x);
-  M = warp_max(M);
-  if (lane == 0) red_m[warp] = M;
-  __syncthreads();
+  float acc[kV] = {}, M = -INFINITY, den = 0.f;
+  for (int s0 = warp; s0 < n; s0 += 256) {
+    const int mine = s0 + 8 * lane, count = min(32, (n - s0 + 7) / 8);
+    const float2 ml = mine < n ? a.part_ml[slot + mine * stride] : make_float2(-INFINITY, 0.f);
+    const float* src = a.part_o + (slot + s0 * stride) * kD + kV * lane;
+    float buf[4][kV];
+    auto load = [&](int i, float (&v)[kV]) {
+      const float* p = src + 8 * i * stride * kD;
+      if (kV == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        v[0] = x.x; v[1] = x.y; v[kV - 2] = x.z; v[kV - 1] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        v[0] = x.x; v[1] = x.y;
+      }
+    };
 #pragma unroll
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, red_m[w]);
-  constexpr int kV = kD / 32;
-  float acc[kV] = {}, den = 0.f;
-  const float mr = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-  for (int s = warp; s < n; s += 8) {
-    const float2 ml = a.part_ml[slot + s * stride];
+    for (int i = 0; i < 4; ++i)
+      if (i < count) load(i, buf[i]);
+    const float top = fmaxf(M, warp_max(ml.x)), mr = top == -INFINITY ? 0.f : top;
+    const float down = ex2(M - mr);  // 0 from -inf
+    M = top;
     const float f = ex2(ml.x - mr);
-    den = fmaf(ml.y, f, den);
-    const float* src = a.part_o + (slot + s * stride) * kD + kV * lane;
-    if (kV == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]);
-      acc[kV - 2] = fmaf(v.z, f, acc[kV - 2]); acc[kV - 1] = fmaf(v.w, f, acc[kV - 1]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]);
+    den = den * down + warp_sum(ml.y * f);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) acc[j] *= down;
+    for (int i0 = 0; i0 < count; i0 += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < count) {
+          const float w = __shfl_sync(0xffffffffu, f, i0 + i);
+#pragma unroll
+          for (int j = 0; j < kV; ++j) acc[j] = fmaf(buf[i][j], w, acc[j]);
+          if (i0 + 4 + i < count) load(i0 + 4 + i, buf[i]);
+        }
     }
   }
 #pragma unroll
-  for (int i = 0; i < kV; ++i) red[warp][kV * lane + i] = acc[i];
-  if (lane == 0) red_l[warp] = den;
+  for (int j = 0; j < kV; ++j) red[warp][kV * lane + j] = acc[j];
+  if (lane == 0) {
+    red_l[warp] = den;
+    red_m[warp] = M;
+  }
   __syncthreads();
   if (threadIdx.x < kD / 2) {
-    float x = 0.f, y = 0.f, l = 0.f;
+    float top = -INFINITY, x = 0.f, y = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, red_m[w]);
+    const float mr = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-      x += red[w][2 * threadIdx.x];
-      y += red[w][2 * threadIdx.x + 1];
-      l += red_l[w];
+      const float f = ex2(red_m[w] - mr);
+      x = fmaf(red[w][2 * threadIdx.x], f, x);
+      y = fmaf(red[w][2 * threadIdx.x + 1], f, y);
+      l = fmaf(red_l[w], f, l);
     }
-    if (a.sink && M != -INFINITY) l += ex2(a.sink[h] * kLog2e - M);
+    if (top != -INFINITY) l += ex2(sink - top);
     const float inv = l != 0.f ? 1.f / l : 0.f;
     uint16_t* dst = reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)row * a.out.row_stride +
                     (int64_t)h * a.out.head_stride + 2 * threadIdx.x;
@@ -771,10 +889,10 @@ __global__ void __launch_bounds__(256) gqa_join_kernel(const DecodeArgs a) {
   }
 }
 
-int most_tiles(const gqa_params& p, int T, int n_max) {
+int most_blocks(const gqa_params& p, int T, int n_max) {
   int64_t keys = n_max;
-  if (p.window > 0 && keys > (int64_t)p.window + T - 1) keys = (int64_t)p.window + T - 1 + kTile - 1;
-  return (int)((keys + kTile - 1) / kTile);
+  if (p.window > 0 && keys > (int64_t)p.window + T - 1) keys = (int64_t)p.window + T - 1 + kBlock - 1;
+  return (int)((keys + kBlock - 1) / kBlock);
 }
 
 template <bool kBf16, bool kFp8, int kD, int kNq>
@@ -792,7 +910,7 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeArg
 }  // namespace
 
 size_t gqa_decode_workspace_bytes(const gqa_params& p, int T, int n_max) {
-  const int s = most_splits(most_tiles(p, T, n_max));
+  const int s = most_splits(most_blocks(p, T, n_max));
   if (s == 1) return 0;
   return (size_t)p.B * s * T * p.n_heads * (p.d + 2) * sizeof(float);
 }
@@ -813,7 +931,7 @@ cudaError_t launch_gqa_decode(const gqa_params& p, const gqa_rows& q, const gqa_
   if (!encode_tensor_map(&mk, dt, 4, cache.k, dims, str, box, sw) ||
       !encode_tensor_map(&mv, dt, 4, cache.v, dims, str, box, sw))
     return cudaErrorInvalidValue;
-  const int splits = most_splits(most_tiles(p, T, n_max));
+  const int splits = most_splits(most_blocks(p, T, n_max));
   const int64_t slots = (int64_t)p.B * splits * T * p.n_heads;
   float* part_o = reinterpret_cast<float*>(ws);
   int shift = 0;
