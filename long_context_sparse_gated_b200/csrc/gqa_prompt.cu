@@ -18,13 +18,26 @@
 //             the other's products.
 //   warps 0-3, 4-7   softmax of unit 0 / 1, a thread a row: the row's 128
 //             logits in registers, running maximum, P in 16 bits back to
-//             TMEM.  The maximum moves only when a row exceeds it by 2^8, so
-//             O is hardly ever rescaled; at the end the same threads
-//             normalise O and write it out through shared memory.
-//   warp 10   looks through the value tiles that some row does not see as a
-//             whole.  Values that are not finite are taken out before the
-//             product (0 * NaN is NaN); where they belong to the sequence,
-//             and so to some of its rows, the units are computed again, row by row.
+//             TMEM, in two halves, so that the product with the first 64 keys
+//             begins while the second half is computed.  The maximum moves
+//             only when a row exceeds it by 2^8, so O is hardly ever rescaled;
+//             at the end the same threads normalise O and write it out
+//             through shared memory.
+//
+// Exponentials.  A tile pair has 32768 of them: 2048 clocks of the 16-lane
+// special-function pipe, as many as its four products take.  So kPoly of
+// every 8 pairs of logits go through the FMA pipe instead: 2^x = 2^n 2^f with n
+// the nearest integer (by adding 1.5 * 2^23) and a polynomial of degree 4 in f
+// (minimax for the relative error on [-1/2, 1/2]: 2.6e-6), n added to the
+// exponent field; weights below 2^-126 of the row's largest come out as about
+// that.  Packed fp32 pairs (f32x2) throughout.
+//
+// Masks.  Tiles that some row does not see as a whole take a path of their
+// own: logits are selected, and the unit's threads look through the value
+// tile.  Values that are not finite are taken out before the product (0 * NaN
+// is NaN); where some row may see them, the units are computed again, row by
+// row.  (One spare warp that looks through all value tiles held the products
+// up: 8 prompts of up to 4096 tokens took 565 us.)
 //
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d columns each).
 // Rounding: P to the activation type (relative 2^-9 or 2^-12); the rest fp32.
@@ -44,6 +57,7 @@ constexpr int kTile = 128;  // query positions of a unit, keys of a tile
 constexpr int kThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;  // base-2 units
+constexpr int kPoly = 3;      // of 8 pairs of exponentials, on the FMA pipe
 
 struct PromptArgs {
   gqa_rows q, k, v, out;
@@ -63,8 +77,8 @@ struct __align__(1024) PromptSmem {
   uint8_t q[2][kOperand];  // later the staged output
   uint8_t k[kK][kOperand];
   uint8_t v[kV][kOperand];
-  uint64_t q_full, k_full[kK], k_empty[kK], v_full[kV], v_ok[kV], v_empty[kV];
-  uint64_t s_full[2], p_full[2], o_full;
+  uint64_t q_full, k_full[kK], k_empty[kK], v_full[kV], v_empty[kV];
+  uint64_t s_full[2], p_full[2][2], o_full;  // p_full: of a unit's half tile
   uint32_t tmem;
   int odd;
   int abort;
@@ -107,14 +121,100 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&u)[
       "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// Whether this lane is the one of its warp that issues MMAs.  The rest of the
+// warp runs along, so that descriptors stay in uniform registers: issued from
+// a branch on the lane index, an MMA took some 118 clocks to issue, twice what
+// it takes to run.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// D[tmem] (+)= A B, 16-bit operands, A in shared memory or TMEM.
+template <bool kAdd>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+               "l"(a), "l"(b), "r"(idesc), "n"(kAdd ? 1 : 0)
+               : "memory");
+}
+template <bool kAdd>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+               "r"(a), "l"(b), "r"(idesc), "n"(kAdd ? 1 : 0)
+               : "memory");
+}
+
+struct True { static constexpr bool value = true; };
+struct False { static constexpr bool value = false; };
+
+// Pairs of fp32 in one register pair.
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x of two numbers that are at most 127 (smaller ones than -126 count as -126).
+__device__ __forceinline__ uint64_t exp2_poly(uint64_t x2) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+  float x, y;
+  split2(x2, x, y);
+  x2 = f32x2(fmaxf(x, -126.f), fmaxf(y, -126.f));
+  const uint64_t t2 = add2(x2, f32x2(kMagic, kMagic));  // the low bits hold round(x)
+  const uint64_t f2 = add2(x2, fma2(add2(t2, f32x2(-kMagic, -kMagic)), f32x2(-1.f, -1.f), 0));
+  uint64_t p2 = fma2(f2, f32x2(0.009570102207362652f, 0.009570102207362652f), f32x2(0.05591785907745361f, 0.05591785907745361f));
+  p2 = fma2(f2, p2, f32x2(0.240247443318367f, 0.240247443318367f));
+  p2 = fma2(f2, p2, f32x2(0.6931217908859253f, 0.6931217908859253f));
+  p2 = fma2(f2, p2, f32x2(0.9999992847442627f, 0.9999992847442627f));
+  float tx, ty;
+  split2(t2, tx, ty);
+  split2(p2, x, y);
+  return f32x2(__int_as_float(__float_as_int(x) + (__float_as_int(tx) << 23)),
+              __int_as_float(__float_as_int(y) + (__float_as_int(ty) << 23)));
+}
+
+// Thread r of 128 looks through its part of a value tile and takes out what is
+// not finite.  True if that was in a row up to `last`.
+template <bool kBf16, int kD>
+__device__ __forceinline__ bool take_out(uint8_t* v, int r, int last) {
+  constexpr uint32_t e = kBf16 ? 0x7F807F80u : 0x7C007C00u, one = kBf16 ? 0x00800080u : 0x04000400u;
+  uint4* v4 = reinterpret_cast<uint4*>(v);
+  uint32_t some = 0;  // an exponent field of all ones carries into the sign's place
+#pragma unroll 4
+  for (int x = r; x < kTile * kD / 8; x += 128) {
+    const uint4 w = v4[x];
+    some |= ((w.x & e) + one) | ((w.y & e) + one) | ((w.z & e) + one) | ((w.w & e) + one);
+  }
+  if (!(some & 0x80008000u)) return false;
+  bool seen = false;
+  for (int x = r; x < kTile * kD / 8; x += 128) {
+    uint32_t w[4] = {v4[x].x, v4[x].y, v4[x].z, v4[x].w};
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t odd = (((w[i] & e) + one) & 0x80008000u) >> 15;
+      any |= odd != 0;
+      w[i] &= ~(odd * 0xFFFFu);
+    }
+    if (any) {
+      v4[x] = make_uint4(w[0], w[1], w[2], w[3]);
+      seen |= ((x >> 3) & (kTile - 1)) <= last;
+    }
+  }
+  sm100::fence_proxy_async_smem();
+  return seen;
 }
 
 // One unit: 128 positions of a query head.
@@ -216,12 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int i = 0; i < Smem::kV; ++i) {
         sm100::mbar_init(&S.v_full[i], 1);
-        sm100::mbar_init(&S.v_ok[i], 1);
         sm100::mbar_init(&S.v_empty[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
         sm100::mbar_init(&S.s_full[i], 1);
-        sm100::mbar_init(&S.p_full[i], 4);
+        sm100::mbar_init(&S.p_full[i][0], 4);
+        sm100::mbar_init(&S.p_full[i][1], 4);
       }
       sm100::mbar_init(&S.o_full, 1);
       sm100::fence_mbar_init();
@@ -302,107 +402,89 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = max(0, n - Smem::kK); i < n; ++i) drain(&S.k_full[i % Smem::kK], (i / Smem::kK) & 1);
         for (int i = max(0, n - Smem::kV); i < n; ++i) drain(&S.v_full[i % Smem::kV], (i / Smem::kV) & 1);
       }
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9) {
       // ---- MMAs
       const uint32_t id_s = kBf16 ? sm100::idesc_bf16(kTile, kTile, 0, 0) : sm100::idesc_f16(kTile, kTile, 0, 0);
       const uint32_t id_o = kBf16 ? sm100::idesc_bf16(kTile, kD, 0, 1) : sm100::idesc_f16(kTile, kD, 0, 1);
       // Q and K K-major (8-row groups 1 KB apart, 64-dim halves 16 KB); V
       // MN-major: 64-dim halves 16 KB apart, groups of 8 keys 1 KB
-      uint64_t dq[2], dk[Smem::kK], dv[Smem::kV];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) dq[i] = sm100::smem_desc(sm100::smem_u32(S.q[i]), 16, 1024, 2);
-#pragma unroll
-      for (int i = 0; i < Smem::kK; ++i) dk[i] = sm100::smem_desc(sm100::smem_u32(S.k[i]), 16, 1024, 2);
-#pragma unroll
-      for (int i = 0; i < Smem::kV; ++i) dv[i] = sm100::smem_desc(sm100::smem_u32(S.v[i]), kTile * 128, 1024, 2);
-      const uint32_t s_col[2] = {tmem, tmem + 128}, o_col[2] = {tmem + 256, tmem + 256 + kD};
+      const uint64_t dq = sm100::smem_desc(sm100::smem_u32(S.q[0]), 16, 1024, 2);
+      const uint64_t dk = sm100::smem_desc(sm100::smem_u32(S.k[0]), 16, 1024, 2);
+      const uint64_t dv = sm100::smem_desc(sm100::smem_u32(S.v[0]), kTile * 128, 1024, 2);
+      const bool leader = elect_one();
       auto active = [&](int i, int j) { return j >= un[i].j0 && j < un[i].j1; };
-      auto issue_s = [&](int i, int n) {  // S_i = Q_i K^T with the n-th K tile
+      auto issue_s = [&](int i, int ks) {  // S_i = Q_i K^T with the K tile of stage ks
         sm100::tc_fence_after();
-        if (!*abort) {
-          uint64_t k = dk[0];
+        if (!*abort && leader) {
+          const uint64_t q = dq + ((i * Smem::kOperand) >> 4), k = dk + ((ks * Smem::kOperand) >> 4);
+          mma_ss<false>(tmem + 128 * i, q, k, id_s);
 #pragma unroll
-          for (int x = 1; x < Smem::kK; ++x)
-            if (n % Smem::kK == x) k = dk[x];
-          const uint64_t q = i ? dq[1] : dq[0];
-#pragma unroll
-          for (int c = 0; c < kD / 16; ++c) {
+          for (int c = 1; c < kD / 16; ++c) {
             const uint32_t off = ((c >> 2) * kTile * 128 + (c & 3) * 32) >> 4;
-            sm100::mma_f16(i ? s_col[1] : s_col[0], q + off, k + off, id_s, c > 0);
+            mma_ss<true>(tmem + 128 * i, q + off, k + off, id_s);
           }
         }
-        sm100::tc_commit(&S.s_full[i]);
+        if (leader) sm100::tc_commit(&S.s_full[i]);
+        __syncwarp();
       };
       if (j_begin < j_end) {
         sm100::mbar_wait_poll(&S.q_full, 0, abort);
         sm100::mbar_wait_poll(&S.k_full[0], 0, abort);
+#pragma unroll
         for (int i = 0; i < 2; ++i)
           if (active(i, j_begin)) issue_s(i, 0);
-        sm100::tc_commit(&S.k_empty[0]);
+        if (leader) sm100::tc_commit(&S.k_empty[0]);
       }
       int done[2] = {0, 0};
-      for (int j = j_begin, n = 0; j < j_end; ++j, ++n) {
-        const int vs = n % Smem::kV;
-        sm100::mbar_wait_poll(&S.v_ok[vs], (n / Smem::kV) & 1, abort);
-        if (j + 1 < j_end) sm100::mbar_wait_poll(&S.k_full[(n + 1) % Smem::kK], ((n + 1) / Smem::kK) & 1, abort);
+      int vs = 0, vph = 0, ks = 1, kph = 0;  // V tile j, K tile j + 1
+      for (int j = j_begin; j < j_end; ++j) {
+        sm100::mbar_wait_poll(&S.v_full[vs], vph, abort);
+        if (j + 1 < j_end) sm100::mbar_wait_poll(&S.k_full[ks], kph, abort);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (active(i, j)) {
-            sm100::mbar_wait_poll(&S.p_full[i], done[i] & 1, abort);
-            sm100::tc_fence_after();
-            if (!*abort) {
-              uint64_t v = dv[0];
+            const uint64_t v = dv + ((vs * Smem::kOperand) >> 4);
+            const uint32_t o_col = tmem + 256 + kD * i, p_col = tmem + 128 * i;
 #pragma unroll
-              for (int x = 1; x < Smem::kV; ++x)
-                if (vs == x) v = dv[x];
+            for (int half = 0; half < 2; ++half) {
+              sm100::mbar_wait_poll(&S.p_full[i][half], done[i] & 1, abort);
+              sm100::tc_fence_after();
+              if (!*abort && leader) {
+                if (half == 0) {
+                  if (done[i] > 0) mma_ts<true>(o_col, p_col, v, id_o);
+                  else mma_ts<false>(o_col, p_col, v, id_o);
+                }
 #pragma unroll
-              for (int c = 0; c < kTile / 16; ++c)
-                mma_f16_ts(o_col[i], s_col[i] + 8 * c, v + ((c * 2048) >> 4), id_o, (done[i] > 0 || c > 0) ? 1u : 0u);
+                for (int c = 4 * half + (half == 0); c < 4 * half + 4; ++c)
+                  mma_ts<true>(o_col, p_col + 8 * c, v + ((c * 2048) >> 4), id_o);
+              }
+              __syncwarp();
             }
             ++done[i];
           }
-          if (active(i, j + 1)) issue_s(i, n + 1);
+          if (active(i, j + 1)) issue_s(i, ks);
         }
-        sm100::tc_commit(&S.v_empty[vs]);
-        if (j + 1 < j_end) sm100::tc_commit(&S.k_empty[(n + 1) % Smem::kK]);
-      }
-      sm100::tc_commit(&S.o_full);
-      if (*abort) {
-        const uint64_t t0 = sm100::globaltimer();
-        while (!sm100::mbar_try_wait(&S.o_full, 0) && sm100::globaltimer() - t0 < sm100::kWaitNs) {
+        if (leader) {
+          sm100::tc_commit(&S.v_empty[vs]);
+          if (j + 1 < j_end) sm100::tc_commit(&S.k_empty[ks]);
+        }
+        __syncwarp();
+        if (++vs == Smem::kV) {
+          vs = 0;
+          vph ^= 1;
+        }
+        if (++ks == Smem::kK) {
+          ks = 0;
+          kph ^= 1;
         }
       }
-    } else if (warp == 10) {
-      // ---- values that are not finite
-      for (int j = j_begin, n = 0; j < j_end; ++j, ++n) {
-        const int vs = n % Smem::kV;
-        sm100::mbar_wait(&S.v_full[vs], (n / Smem::kV) & 1, abort);
-        if (edge_of(un[0], j) || edge_of(un[1], j)) {
-          constexpr uint32_t e = kBf16 ? 0x7F80u : 0x7C00u;
-          bool own = false, any = false;
-          uint4* v4 = reinterpret_cast<uint4*>(S.v[vs]);
-#pragma unroll 4
-          for (int x = lane; x < Smem::kOperand / 16; x += 32) {
-            uint4 w = v4[x];
-            uint32_t bad[4];
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-            uint32_t some = 0;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              bad[y] = ((in[y] & e) == e ? 0xFFFFu : 0u) | ((in[y] & (e << 16)) == (e << 16) ? 0xFFFF0000u : 0u);
-              some |= bad[y];
-            }
-            if (some) {
-              v4[x] = make_uint4(w.x & ~bad[0], w.y & ~bad[1], w.z & ~bad[2], w.w & ~bad[3]);
-              any = true;
-              own |= j * kTile + ((x >> 3) & (kTile - 1)) <= max(un[0].t1, un[1].t1);  // a key that some row may see
-            }
+      if (leader) {
+        sm100::tc_commit(&S.o_full);
+        if (*abort) {
+          const uint64_t t0 = sm100::globaltimer();
+          while (!sm100::mbar_try_wait(&S.o_full, 0) && sm100::globaltimer() - t0 < sm100::kWaitNs) {
           }
-          if (own) S.odd = 1;
-          if (any) sm100::fence_proxy_async_smem();
-          __syncwarp();
         }
-        if (lane == 0) sm100::mbar_arrive(&S.v_ok[vs]);
       }
     }
   } else {
@@ -426,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::tmem_ld_wait();
 #pragma unroll
       for (int c = 0; c < 128; c += 32) pin32(s, c);
-      if (edge_of(u, u.j0 + n)) {
+      const bool edge = edge_of(u, u.j0 + n);
+      if (edge) {
         const int hi = t - key0, lo = a.window > 0 ? t - a.window - key0 : INT32_MIN;  // seen: lo < c <= hi
 #pragma unroll
         for (int c = 0; c < 128; ++c)
@@ -457,25 +540,49 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const float mc = m == -INFINITY ? 0.f : m * a.scale;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t p[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float x = ex2(fmaf(s[64 * half + 2 * c], a.scale, -mc)), y = ex2(fmaf(s[64 * half + 2 * c + 1], a.scale, -mc));
-          sum[(2 * c) & 3] += x;
-          sum[(2 * c + 1) & 3] += y;
-          p[c] = pack2<kBf16>(x, y);
-        }
-        tmem_st_x32(s_col + 32 * half, p);
+      if (edge) {
+        // (S being here says that the loads of all earlier tiles have been
+        // waited for, so this parity cannot mean an earlier one)
+        const int nu = u.j0 + n - j_begin, vs = nu % Smem::kV;
+        sm100::mbar_wait(&S.v_full[vs], (nu / Smem::kV) & 1, abort);
+        if (take_out<kBf16, kD>(S.v[vs], r, max(un[0].t1, un[1].t1) - key0)) S.odd = 1;
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      sm100::tmem_st_wait();
-      sm100::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(&S.p_full[i]);
+      const float mc = m == -INFINITY ? 0.f : m * a.scale;
+      const uint64_t scale2 = f32x2(a.scale, a.scale), mc2 = f32x2(-mc, -mc);
+      uint64_t sum2[2] = {0, 0};
+      auto weights = [&](auto poly) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint64_t x2 = fma2(f32x2(s[64 * half + 2 * c], s[64 * half + 2 * c + 1]), scale2, mc2);
+            float x, y;
+            if (decltype(poly)::value && (c * kPoly) % 8 < kPoly) {
+              const uint64_t y2 = exp2_poly(x2);
+              split2(y2, x, y);
+              sum2[c & 1] = add2(sum2[c & 1], y2);
+            } else {
+              split2(x2, x, y);
+              x = ex2(x);
+              y = ex2(y);
+              sum2[c & 1] = add2(sum2[c & 1], f32x2(x, y));
+            }
+            p[c] = pack2<kBf16>(x, y);
+          }
+          tmem_st_x32(s_col + 32 * half, p);
+          sm100::tmem_st_wait();
+          sm100::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) sm100::mbar_arrive(&S.p_full[i][half]);
+        }
+      };
+      if (edge) weights(False{});  // masked weights have to be zeros
+      else weights(True{});
+      float a0, a1, a2, a3;
+      split2(sum2[0], a0, a1);
+      split2(sum2[1], a2, a3);
+      l += (a0 + a1) + (a2 + a3);
     }
 
     // ---- output
