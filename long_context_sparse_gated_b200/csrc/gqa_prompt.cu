@@ -57,7 +57,7 @@ constexpr int kTile = 128;  // query positions of a unit, keys of a tile
 constexpr int kThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;  // base-2 units
-constexpr int kPoly = 3;      // of 8 pairs of exponentials, on the FMA pipe
+constexpr int kPoly = 2;      // of 8 pairs of exponentials, on the FMA pipe
 
 struct PromptArgs {
   gqa_rows q, k, v, out;
@@ -144,6 +144,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
                : "memory");
 }
 
+// Barrier over a unit's 128 threads that tells them whether one of them said so.
+__device__ __forceinline__ bool unit_any(int unit, bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)mine), "r"(1 + unit)
+      : "memory");
+  return r != 0;
+}
+
 struct True { static constexpr bool value = true; };
 struct False { static constexpr bool value = false; };
 
@@ -173,7 +184,7 @@ __device__ __forceinline__ uint64_t exp2_poly(uint64_t x2) {
   split2(x2, x, y);
   x2 = f32x2(fmaxf(x, -126.f), fmaxf(y, -126.f));
   const uint64_t t2 = add2(x2, f32x2(kMagic, kMagic));  // the low bits hold round(x)
-  const uint64_t f2 = add2(x2, fma2(add2(t2, f32x2(-kMagic, -kMagic)), f32x2(-1.f, -1.f), 0));
+  const uint64_t f2 = fma2(add2(t2, f32x2(-kMagic, -kMagic)), f32x2(-1.f, -1.f), x2);
   uint64_t p2 = fma2(f2, f32x2(0.009570102207362652f, 0.009570102207362652f), f32x2(0.05591785907745361f, 0.05591785907745361f));
   p2 = fma2(f2, p2, f32x2(0.240247443318367f, 0.240247443318367f));
   p2 = fma2(f2, p2, f32x2(0.6931217908859253f, 0.6931217908859253f));
@@ -625,12 +636,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(dst) = stage[row * kChunks + (ch ^ (row & 7))];
           }
         }
-        if (*reinterpret_cast<volatile int*>(&S.odd)) {
-          // all four warps have written their rows before others rewrite them
-          sm100::named_bar_sync(1 + i, 128);
-          unit_by_rows<kBf16, kD>(a, u, kvh, k_begin, warp & 3, lane);
-        }
       }
+      // (all four warps have written their rows before others rewrite them)
+      if (work > 0 && unit_any(i, *reinterpret_cast<volatile int*>(&S.odd) != 0))
+        unit_by_rows<kBf16, kD>(a, u, kvh, k_begin, warp & 3, lane);
     }
   }
   __syncwarp();
