@@ -32,12 +32,13 @@
 // exponent field; weights below 2^-126 of the row's largest come out as about
 // that.  Packed fp32 pairs (f32x2) throughout.
 //
-// Masks.  Tiles that some row does not see as a whole take a path of their
-// own: logits are selected, and the unit's threads look through the value
-// tile.  Values that are not finite are taken out before the product (0 * NaN
-// is NaN); where some row may see them, the units are computed again, row by
-// row.  (One spare warp that looks through all value tiles held the products
-// up: 8 prompts of up to 4096 tokens took 565 us.)
+// Masks.  In tiles that some row does not see as a whole logits are selected,
+// blocks of 32 keys that a warp's rows all see or all miss at once.  A value
+// that is not finite where a row's weight is 0 would still reach the row's sum
+// (0 * NaN is NaN): rows behind the sequence are cleared in shared memory, and
+// a row that comes out as something not finite is computed again on its own,
+// from the keys it sees.  (Looking through the value tiles before the products
+// cost 2700 clocks a tile.)
 //
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d columns each).
 // Rounding: P to the activation type (relative 2^-9 or 2^-12); the rest fp32.
@@ -80,9 +81,8 @@ struct __align__(1024) PromptSmem {
   uint64_t q_full, k_full[kK], k_empty[kK], v_full[kV], v_empty[kV];
   uint64_t s_full[2], p_full[2][2], o_full;  // p_full: of a unit's half tile
   uint32_t tmem;
-  int odd;
   int abort;
-  int item[4];  // sequence, pair of units, KV head
+  int item[6];  // sequence (-1: none), its block, first query, queries, first key, keys
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -144,17 +144,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
                : "memory");
 }
 
-// Barrier over a unit's 128 threads that tells them whether one of them said so.
-__device__ __forceinline__ bool unit_any(int unit, bool mine) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)mine), "r"(1 + unit)
-      : "memory");
-  return r != 0;
-}
-
 struct True { static constexpr bool value = true; };
 struct False { static constexpr bool value = false; };
 
@@ -196,36 +185,12 @@ __device__ __forceinline__ uint64_t exp2_poly(uint64_t x2) {
               __int_as_float(__float_as_int(y) + (__float_as_int(ty) << 23)));
 }
 
-// Thread r of 128 looks through its part of a value tile and takes out what is
-// not finite.  True if that was in a row up to `last`.
-template <bool kBf16, int kD>
-__device__ __forceinline__ bool take_out(uint8_t* v, int r, int last) {
-  constexpr uint32_t e = kBf16 ? 0x7F807F80u : 0x7C007C00u, one = kBf16 ? 0x00800080u : 0x04000400u;
-  uint4* v4 = reinterpret_cast<uint4*>(v);
-  uint32_t some = 0;  // an exponent field of all ones carries into the sign's place
-#pragma unroll 4
-  for (int x = r; x < kTile * kD / 8; x += 128) {
-    const uint4 w = v4[x];
-    some |= ((w.x & e) + one) | ((w.y & e) + one) | ((w.z & e) + one) | ((w.w & e) + one);
-  }
-  if (!(some & 0x80008000u)) return false;
-  bool seen = false;
-  for (int x = r; x < kTile * kD / 8; x += 128) {
-    uint32_t w[4] = {v4[x].x, v4[x].y, v4[x].z, v4[x].w};
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t odd = (((w[i] & e) + one) & 0x80008000u) >> 15;
-      any |= odd != 0;
-      w[i] &= ~(odd * 0xFFFFu);
-    }
-    if (any) {
-      v4[x] = make_uint4(w[0], w[1], w[2], w[3]);
-      seen |= ((x >> 3) & (kTile - 1)) <= last;
-    }
-  }
+// Thread r of 128 clears its part of the rows from `first` on of a value tile.
+template <int kD>
+__device__ __forceinline__ void clear_rows(uint8_t* v, int r, int first) {
+  for (int x = r; x < kTile * kD / 8; x += 128)
+    if (((x >> 3) & (kTile - 1)) >= first) reinterpret_cast<uint4*>(v)[x] = make_uint4(0, 0, 0, 0);
   sm100::fence_proxy_async_smem();
-  return seen;
 }
 
 // One unit: 128 positions of a query head.
@@ -236,10 +201,10 @@ struct Unit {
   int j0, j1;      // key tiles [j0, j1)
 };
 
-// The rows of a unit one by one, a warp a row: the path for values that are
-// not finite and belong to some of the rows.
+// Row r of a unit on its own, by a warp: the path for rows that came out as
+// something not finite.
 template <bool kBf16, int kD>
-__device__ __noinline__ void unit_by_rows(const PromptArgs& a, const Unit& u, int kvh, int k0, int warp, int lane) {
+__device__ __noinline__ void one_row(const PromptArgs& a, const Unit& u, int kvh, int k0, int r, int lane) {
   constexpr int n = kD / 32;
   auto load = [&](const gqa_rows& s, int64_t row, int h, float (&x)[n]) {
 #pragma unroll
@@ -250,30 +215,28 @@ __device__ __noinline__ void unit_by_rows(const PromptArgs& a, const Unit& u, in
       x[j + 1] = f.y;
     }
   };
-  for (int r = warp; r < u.rows; r += 4) {
-    const int t = u.t0 + r, first = a.window > 0 ? max(0, t - a.window + 1) : 0;
-    float q[n], x[n], o[n] = {}, m = -INFINITY, l = 0.f;
-    load(a.q, u.row0 + r, u.head, q);
-    for (int j = first; j <= t; ++j) {
-      load(a.k, k0 + j, kvh, x);
-      float z = 0.f;
+  const int t = u.t0 + r, first = a.window > 0 ? max(0, t - a.window + 1) : 0;
+  float q[n], x[n], o[n] = {}, m = -INFINITY, l = 0.f;
+  load(a.q, u.row0 + r, u.head, q);
+  for (int j = first; j <= t; ++j) {
+    load(a.k, k0 + j, kvh, x);
+    float z = 0.f;
 #pragma unroll
-      for (int e = 0; e < n; ++e) z = fmaf(q[e], x[e], z);
-      z = warp_sum(z) * a.scale;
-      const float mn = fmaxf(m, z), f = m == -INFINITY ? 0.f : ex2(m - mn), p = ex2(z - mn);
-      load(a.v, k0 + j, kvh, x);
-      l = l * f + p;
+    for (int e = 0; e < n; ++e) z = fmaf(q[e], x[e], z);
+    z = warp_sum(z) * a.scale;
+    const float mn = fmaxf(m, z), f = m == -INFINITY ? 0.f : ex2(m - mn), p = ex2(z - mn);
+    load(a.v, k0 + j, kvh, x);
+    l = l * f + p;
 #pragma unroll
-      for (int e = 0; e < n; ++e) o[e] = fmaf(p, x[e], f == 0.f ? 0.f : o[e] * f);
-      m = mn;
-    }
-    if (a.sink && m != -INFINITY) l += ex2(a.sink[u.head] * kLog2e - m);
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < n; e += 2)
-      *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)(u.row0 + r) * a.out.row_stride +
-                                   u.head * a.out.head_stride + n * lane + e) = pack2<kBf16>(o[e] * inv, o[e + 1] * inv);
+    for (int e = 0; e < n; ++e) o[e] = fmaf(p, x[e], f == 0.f ? 0.f : o[e] * f);
+    m = mn;
   }
+  if (a.sink && m != -INFINITY) l += ex2(a.sink[u.head] * kLog2e - m);
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < n; e += 2)
+    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)(u.row0 + r) * a.out.row_stride +
+                                 u.head * a.out.head_stride + n * lane + e) = pack2<kBf16>(o[e] * inv, o[e + 1] * inv);
 }
 
 template <bool kBf16, int kD>
@@ -286,15 +249,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &S.abort;
 
+  if (warp == 8) {
+    sm100::tmem_alloc(&S.tmem, 512);
+    sm100::tmem_relinquish();
+    sm100::tc_fence_before();
+  }
   pdl_wait();
   // ---- which sequence, pair of units and KV head
   const int G = a.n_heads / a.n_kv;
   if (warp == 0) {
     int base = 0, found = -1, rest = 0;
     for (int b0 = 0; b0 < a.B && found < 0; b0 += 32) {
-      int n = 0;
+      int n = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
       if (b0 + lane < a.B) {
-        const int q0 = a.cu_q[b0 + lane], q1 = a.cu_q[b0 + lane + 1], k0 = a.cu_k[b0 + lane], k1 = a.cu_k[b0 + lane + 1];
+        q0 = a.cu_q[b0 + lane];
+        q1 = a.cu_q[b0 + lane + 1];
+        k0 = a.cu_k[b0 + lane];
+        k1 = a.cu_k[b0 + lane + 1];
         if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k) {
           if (blockIdx.x == 0) raise_err(a.err, CSA_DEV_ERR_RANGE);
         } else {
@@ -311,14 +282,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned hit = __ballot_sync(0xffffffffu, at >= 0 && at < n);
       if (hit) {
         found = b0 + __ffs(hit) - 1;
-        rest = __shfl_sync(0xffffffffu, at, __ffs(hit) - 1);
+        const int src = __ffs(hit) - 1;
+        rest = __shfl_sync(0xffffffffu, at, src);
+        const int w0 = __shfl_sync(0xffffffffu, q0, src), w1 = __shfl_sync(0xffffffffu, q1, src);
+        const int w2 = __shfl_sync(0xffffffffu, k0, src), w3 = __shfl_sync(0xffffffffu, k1, src);
+        if (lane == 0) {
+          S.item[2] = w0;
+          S.item[3] = w1 - w0;
+          S.item[4] = w2;
+          S.item[5] = w3 - w2;
+        }
       }
       base += __shfl_sync(0xffffffffu, x, 31);
     }
     if (lane == 0) {
       S.item[0] = found;
       S.item[1] = rest;
-      S.odd = 0;
       S.abort = 0;
       sm100::mbar_init(&S.q_full, 1);
       for (int i = 0; i < Smem::kK; ++i) {
@@ -331,17 +310,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int i = 0; i < 2; ++i) {
         sm100::mbar_init(&S.s_full[i], 1);
-        sm100::mbar_init(&S.p_full[i][0], 4);
-        sm100::mbar_init(&S.p_full[i][1], 4);
+        for (int x = 0; x < 2; ++x) sm100::mbar_init(&S.p_full[i][x], 4);
       }
       sm100::mbar_init(&S.o_full, 1);
       sm100::fence_mbar_init();
     }
   }
   __syncthreads();
-  const int b = S.item[0];
-  if (b < 0) return;
-  const int q_begin = a.cu_q[b], n_q = a.cu_q[b + 1] - q_begin, k_begin = a.cu_k[b], n_k = a.cu_k[b + 1] - k_begin;
+  sm100::tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  if (S.item[0] < 0) {
+    if (warp == 8) sm100::tmem_dealloc(tmem, 512);
+    return;
+  }
+  const int q_begin = S.item[2], n_q = S.item[3], k_begin = S.item[4], n_k = S.item[5];
   const int tiles = (n_q + kTile - 1) / kTile, pairs = (tiles * G + 1) / 2;
   const int kvh = S.item[1] % a.n_kv, pair = pairs - 1 - S.item[1] / a.n_kv;
   Unit un[2];
@@ -365,15 +347,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto edge_of = [&](const Unit& u, int j) {
     return j >= u.j0 && j < u.j1 && (j * kTile + kTile - 1 > u.t0 || (a.window > 0 && j * kTile <= u.t1 - a.window));
   };
-
-  if (warp == 8) {
-    sm100::tmem_alloc(&S.tmem, 512);
-    sm100::tmem_relinquish();
-  }
-  sm100::tc_fence_before();
-  __syncthreads();
-  sm100::tc_fence_after();
-  const uint32_t tmem = S.tmem;
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -520,11 +493,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 128; c += 32) pin32(s, c);
       const bool edge = edge_of(u, u.j0 + n);
+      uint32_t none = 0;  // blocks of 32 keys that no row of the warp sees
       if (edge) {
-        const int hi = t - key0, lo = a.window > 0 ? t - a.window - key0 : INT32_MIN;  // seen: lo < c <= hi
+        // columns lo < c <= hi are seen; a warp's rows lie 31 apart at most, so
+        // that most blocks are seen by all of them or by none
+        const int hi = t - key0, lo = a.window > 0 ? t - a.window - key0 : INT32_MIN;
+        const int hi0 = hi - lane, lo0 = a.window > 0 ? lo - lane : INT32_MIN, lo1 = a.window > 0 ? lo0 + 31 : INT32_MIN;
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > hi || c <= lo) s[c] = -INFINITY;
+        for (int k = 0; k < 4; ++k) {
+          if (32 * k > hi0 + 31 || 32 * k + 31 <= lo0) {
+            none |= 1u << k;
+#pragma unroll
+            for (int c = 32 * k; c < 32 * k + 32; ++c) s[c] = -INFINITY;
+          } else {
+            if (32 * k + 31 > hi0) {
+#pragma unroll
+              for (int c = 32 * k; c < 32 * k + 32; ++c)
+                if (c > hi) s[c] = -INFINITY;
+            }
+            if (32 * k <= lo1) {
+#pragma unroll
+              for (int c = 32 * k; c < 32 * k + 32; ++c)
+                if (c <= lo) s[c] = -INFINITY;
+            }
+          }
+        }
+        if (key0 + kTile > n_k) {
+          // rows behind the sequence: cleared, since 0 * NaN is NaN.  (S being
+          // here says that the loads of all earlier tiles have been waited
+          // for, so this parity cannot mean an earlier one)
+          const int nu = u.j0 + n - j_begin, vs = nu % Smem::kV;
+          sm100::mbar_wait(&S.v_full[vs], (nu / Smem::kV) & 1, abort);
+          clear_rows<kD>(S.v[vs], r, n_k - key0);
+        }
       }
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -551,13 +552,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (edge) {
-        // (S being here says that the loads of all earlier tiles have been
-        // waited for, so this parity cannot mean an earlier one)
-        const int nu = u.j0 + n - j_begin, vs = nu % Smem::kV;
-        sm100::mbar_wait(&S.v_full[vs], (nu / Smem::kV) & 1, abort);
-        if (take_out<kBf16, kD>(S.v[vs], r, max(un[0].t1, un[1].t1) - key0)) S.odd = 1;
-      }
       const float mc = m == -INFINITY ? 0.f : m * a.scale;
       const uint64_t scale2 = f32x2(a.scale, a.scale), mc2 = f32x2(-mc, -mc);
       uint64_t sum2[2] = {0, 0};
@@ -567,6 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t p[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
+            if (!decltype(poly)::value && ((none >> (2 * half + c / 16)) & 1)) {
+              p[c] = 0;
+              continue;
+            }
             const uint64_t x2 = fma2(f32x2(s[64 * half + 2 * c], s[64 * half + 2 * c + 1]), scale2, mc2);
             float x, y;
             if (decltype(poly)::value && (c * kPoly) % 8 < kPoly) {
@@ -604,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (u.rows > 0) {
       if (a.sink && m != -INFINITY) l += ex2(a.sink[u.head] * kLog2e - m * a.scale);
       const float f = l != 0.f ? 1.f / l : 0.f;
+      uint32_t top = 0;  // largest magnitude of the row, as bits
       constexpr int kChunks = kD / 8;  // 16-byte pieces of a row
       uint4* stage = reinterpret_cast<uint4*>(S.q[i]) + (warp & 3) * 32 * kChunks;  // the warp's 32 rows
 #pragma unroll
@@ -621,7 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h) {
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[8 * h + e]) * f;
+          for (int e = 0; e < 8; ++e) {
+            x[e] = __uint_as_float(w[8 * h + e]) * f;
+            top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+          }
           stage[lane * kChunks + ((c / 8 + h) ^ (lane & 7))] = pack8<kBf16>(x);
         }
       }
@@ -636,10 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(dst) = stage[row * kChunks + (ch ^ (row & 7))];
           }
         }
+        __syncwarp();
+        for (unsigned odd = __ballot_sync(0xffffffffu, r < u.rows && top >= 0x7F800000u); odd; odd &= odd - 1)
+          one_row<kBf16, kD>(a, u, kvh, k_begin, (warp & 3) * 32 + __ffs(odd) - 1, lane);
       }
-      // (all four warps have written their rows before others rewrite them)
-      if (work > 0 && unit_any(i, *reinterpret_cast<volatile int*>(&S.odd) != 0))
-        unit_by_rows<kBf16, kD>(a, u, kvh, k_begin, warp & 3, lane);
     }
   }
   __syncwarp();
