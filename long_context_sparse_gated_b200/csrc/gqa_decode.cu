@@ -67,6 +67,9 @@ constexpr int kBlock = 32;  // keys: splits begin at multiples of it
 constexpr int kMaxStages = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;      // base-2 units
+constexpr float kNone = -3.0e38f;  // a running maximum before the first key
+struct Edge { static constexpr bool value = true; };
+struct Whole { static constexpr bool value = false; };
 constexpr float kMinLogScale = -90.f, kMaxLogScale = 90.f;
 
 // Blocks per split for a sequence of n blocks: about 32 splits of 4 to 16
@@ -100,7 +103,7 @@ struct DecodeArgs {
   float* part_o;   // [B][max_splits][T * n_heads][d]
   float2* part_ml; // [B][max_splits][T * n_heads]: (m, l), m in base-2 units
   int64_t n_pages;
-  int B, T, n_max, n_heads, n_kv, page, page_shift, window, max_splits;
+  int B, T, n_max, n_heads, n_kv, kv_shift, page, page_shift, window, max_splits;  // kv_shift: log2 n_kv, or -1
   float scale;  // softmax_scale * log2(e)
   int32_t* err;
 };
@@ -170,15 +173,24 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return v;
 }
 
-// A box of K or V: 16 rows of one page and head, the 64-dim halves of a
+// K or V of a tile: 16 rows of one page and head, the 64-dim halves of a
 // 16-bit row one after the other.
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
-          "r"(sm100::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(sm100::smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // Two E4M3 codes (low 16 bits) -> two FP16.
 __device__ __forceinline__ uint32_t cvt_codes(uint32_t v) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
@@ -305,14 +317,15 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
   float* scales = reinterpret_cast<float*>(all + L::kSlots * L::kStage + warp * n_st * L::kScales);
   float4* join = reinterpret_cast<float4*>(all + L::kSlots * (L::kStage + L::kScales) + team * L::kJoin);
   uint64_t* full = full_bar + warp * n_st;
+  const uint32_t ring_u32 = sm100::smem_u32(ring), scales_u32 = sm100::smem_u32(scales), full_u32 = sm100::smem_u32(full);
   volatile int* abort = &abort_flag;
 
   auto enter = [&](Item& c, int item) {
     while (item >= first_item[c.at + 1]) ++c.at;
     c.b = order[c.at];
-    const int in_b = item - first_item[c.at], x = in_b / chunks;
+    const int in_b = item - first_item[c.at], x = chunks == 1 ? in_b : in_b / chunks;
     c.chunk = in_b - x * chunks;
-    c.split = x / a.n_kv;
+    c.split = a.kv_shift >= 0 ? x >> a.kv_shift : x / a.n_kv;
     c.kvh = x - c.split * a.n_kv;
     c.s = span_of(a, c.b);
     const int n = split_blocks(c.s.n), b0 = c.s.b0 + c.split * n;
@@ -355,17 +368,18 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
       const int st = st_ld;
       none = id >= 0 ? none & ~(1u << st) : none | (1u << st);
       if (lane == 0) {
+        const uint32_t bar = full_u32 + 8 * st;
         if (id >= 0) {
-          sm100::mbar_arrive_expect_tx(&full[st], L::kStage + L::kScales);
-          uint8_t* dst = ring + st * L::kStage;
+          expect_tx(bar, L::kStage + L::kScales);
+          const uint32_t dst = ring_u32 + st * L::kStage;
           const int slot = key & (a.page - 1), head_page = id * a.n_kv + ld.kvh;
-          tma_load_4d(dst, &map_k, &full[st], 0, slot, 0, head_page);
-          tma_load_4d(dst + L::kOperand, &map_v, &full[st], 0, slot, 0, head_page);
+          tma_load_4d(dst, &map_k, bar, 0, slot, 0, head_page);
+          tma_load_4d(dst + L::kOperand, &map_v, bar, 0, slot, 0, head_page);
           if (kFp8) {
-            const int64_t at = (int64_t)head_page * a.page + slot;
-            float* sc = scales + st * 2 * kTile;
-            sm100::bulk_load(sc, a.k_scale + at, kTile * 4, &full[st]);
-            sm100::bulk_load(sc + kTile, a.v_scale + at, kTile * 4, &full[st]);
+            const int64_t at = ((int64_t)head_page << a.page_shift) + slot;
+            const uint32_t sc = scales_u32 + st * L::kScales;
+            bulk_load(sc, a.k_scale + at, kTile * 4, bar);
+            bulk_load(sc + kTile * 4, a.v_scale + at, kTile * 4, bar);
           }
         } else {
           sm100::mbar_arrive(&full[st]);
@@ -452,7 +466,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
     float m[kNt][2], l[kNt][2], o[kD / 16][kNt][4];
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kNone;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int mt = 0; mt < kD / 16; ++mt)
@@ -466,14 +480,16 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
       if (!((none >> st) & 1)) {
         const int key0 = c.t * kTile;
         const uint32_t sk = sm100::smem_u32(ring + st * L::kStage), sv = sk + L::kOperand;
-        // not seen by every row: keys after the first query, before the last
-        // query's window
-        const bool edge = key0 + kTile - 1 > c.s.len - a.T || (a.window > 0 && key0 < c.s.len - a.window);
+        // some row does not see it as a whole: keys after the first query, or
+        // before the last query's window
+        const bool at_edge = key0 + kTile - 1 > c.s.len - a.T || (a.window > 0 && key0 < c.s.len - a.window);
         auto seen = [&](int k, int tcol) {  // the tile's k-th key
           const int key = key0 + k;
           return key <= tcol && (a.window == 0 || key > tcol - a.window);
         };
 
+        auto tile = [&](auto kind) {
+        constexpr bool edge = decltype(kind)::value;
         // S^T = K Q^T (keys g, g + 8), in two chains of MMAs
         float z[kNt][4], z2[kNt][4];
 #pragma unroll
@@ -551,7 +567,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
               alpha[e] = 1.f;
               if (v > m[nt][e]) {
-                alpha[e] = ex2(m[nt][e] - v);  // 0 from -inf
+                alpha[e] = ex2(m[nt][e] - v);  // 0 from kNone
                 m[nt][e] = v;
               }
               l[nt][e] *= alpha[e];
@@ -570,7 +586,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float u = z[nt][e];
-            p[e] = ex2(u - (m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1]));
+            p[e] = ex2(u - m[nt][e & 1]);
             if (!kFp8) l[nt][e & 1] += p[e];
             else if (!edge || u != -INFINITY) l[nt][e & 1] = fmaf(p[e], rv[e >> 1], l[nt][e & 1]);
           }
@@ -657,6 +673,9 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
               }
             }
         }
+        };
+        if (at_edge) tile(Edge{});
+        else tile(Whole{});
       }
       __syncwarp();  // every lane has read the stage
       ++done;
@@ -673,6 +692,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
     for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        if (m[nt][e] == kNone) m[nt][e] = -INFINITY;
         float v = l[nt][e];
         v += __shfl_xor_sync(0xffffffffu, v, 4);
         v += __shfl_xor_sync(0xffffffffu, v, 8);
@@ -936,9 +956,12 @@ cudaError_t launch_gqa_decode(const gqa_params& p, const gqa_rows& q, const gqa_
   float* part_o = reinterpret_cast<float*>(ws);
   int shift = 0;
   while ((1 << shift) < p.page) ++shift;
+  int kv_shift = 0;
+  while ((1 << kv_shift) < p.n_kv_heads) ++kv_shift;
+  if ((1 << kv_shift) != p.n_kv_heads) kv_shift = -1;
   const DecodeArgs a{q, out, cache.k_scale, cache.v_scale, table, table_cols, lens, sink, part_o,
                      splits > 1 ? reinterpret_cast<float2*>(part_o + slots * p.d) : nullptr, cache.n_pages, p.B, T,
-                     n_max, p.n_heads, p.n_kv_heads, p.page, shift, p.window, splits, p.softmax_scale * kLog2e, err};
+                     n_max, p.n_heads, p.n_kv_heads, kv_shift, p.page, shift, p.window, splits, p.softmax_scale * kLog2e, err};
   // 8 query rows per item where they hold the whole group, else 16
   const int rows = T * (p.n_heads / p.n_kv_heads), nq = rows <= 8 ? 8 : 16;
   const int64_t items = (int64_t)p.B * splits * p.n_kv_heads * ((rows + nq - 1) / nq);
