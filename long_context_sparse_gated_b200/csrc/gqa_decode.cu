@@ -72,12 +72,17 @@ struct Edge { static constexpr bool value = true; };
 struct Whole { static constexpr bool value = false; };
 constexpr float kMinLogScale = -90.f, kMaxLogScale = 90.f;
 
-// Blocks per split for a sequence of n blocks: about 32 splits of 4 to 16
-// blocks (128 to 512 keys).
-constexpr int kMinSplit = 4, kMaxSplit = 16, kSplits = 32;
+// Blocks per split for a sequence of n blocks: 8, 16 or 32 blocks, so that
+// there are about 12 splits (256 to 1024 keys), and 64 for more than 64K keys.
+// Measured (single 777 keys / 32 mixed up to 16K / 4 of 128K / 24 FP8 up to
+// 32K / 16 x 4 drafted tokens, us): this 14.1 / 153 / 327 / 177 / 16; 4 to 16 blocks
+// and 32 splits 13.8 / 165 / 357 / 201 / 20; up to 32 blocks throughout - / 153 / 346 /
+// 177 / 16; from 16 blocks on 16.4 / 152 / 328 / 179 / 17.
+constexpr int kMinSplit = 8, kMidSplit = 32, kMaxSplit = 64, kSplits = 12, kLong = 2048;
 __host__ __device__ inline int split_blocks(int n) {
+  if (n > kLong) return kMaxSplit;
   int c = kMinSplit;
-  while (c < kMaxSplit && c * kSplits < n) c *= 2;
+  while (c < kMidSplit && c * kSplits < n) c *= 2;
   return c;
 }
 __host__ __device__ inline int n_splits(int n) {
@@ -87,8 +92,8 @@ __host__ __device__ inline int n_splits(int n) {
 // The most splits that any sequence of up to n blocks has.
 inline int most_splits(int n) {
   int most = n_splits(n);
-  for (int c = kMinSplit; c < kMaxSplit; c *= 2)  // the longest sequence cut into c blocks
-    if (c * kSplits < n && most < kSplits) most = kSplits;
+  for (int top : {kMinSplit * kSplits, 2 * kMinSplit * kSplits, kLong})  // the longest of their kind
+    if (top < n && most < n_splits(top)) most = n_splits(top);
   return most;
 }
 
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
   int* counts = reinterpret_cast<int*>(all);
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
     const int n = span_of(a, b).n;
-    counts[b] = n_splits(n) * 32 + split_blocks(n);
+    counts[b] = n_splits(n) * 128 + split_blocks(n);
     if (blockIdx.x == 0 && a.lens[b] > a.n_max) raise_err(a.err, CSA_DEV_ERR_RANGE);
   }
   __syncthreads();
@@ -283,10 +288,10 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
     for (int c = kMaxSplit; c >= kMinSplit; c /= 2)
       for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int x = b0 + lane < a.B ? counts[b0 + lane] : 0;
-        const bool mine = (x & 31) == c;
+        const bool mine = (x & 127) == c;
         const unsigned who = __ballot_sync(0xffffffffu, mine);
         if (!who) continue;
-        const int n = mine ? (x >> 5) * a.n_kv * chunks : 0;
+        const int n = mine ? (x >> 7) * a.n_kv * chunks : 0;
         int sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
