@@ -118,9 +118,9 @@ struct DecodeArgs {
 struct Span {
   int len, lo, b0, n;
 };
-__device__ __forceinline__ Span span_of(const DecodeArgs& a, int b) {
+__device__ __forceinline__ Span span_of(const DecodeArgs& a, int len) {
   Span s;
-  s.len = max(0, min(a.lens[b], a.n_max));
+  s.len = max(0, min(len, a.n_max));
   s.lo = a.window > 0 ? max(0, s.len - a.T - a.window + 1) : 0;
   s.b0 = s.lo / kBlock;
   s.n = s.len > s.lo ? (s.len + kBlock - 1) / kBlock - s.b0 : 0;
@@ -223,20 +223,22 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t v) {
 }
 
 constexpr int kTeam = 4;  // warps
-constexpr int kMaxB = 1024;
+constexpr int kMaxB = 1024, kNear = 256;
 
 template <bool kFp8, int kD, int kNq>
 struct Layout {
-  // three teams of up to 168 registers a thread, or two of up to 255
-  static constexpr int kTeams = kNq == 8 ? 3 : 2, kWarps = kTeam * kTeams;
+  // 8 query rows: three teams of up to 168 registers a thread, or four of 128 for
+  // an FP8 cache, whose work is in the instructions (184 us with three, 167 with
+  // four, 218 with two); 16 rows: two of up to 255
+  static constexpr int kTeams = kNq == 8 ? (kFp8 ? 4 : 3) : 2, kWarps = kTeam * kTeams;
   static constexpr int kRowBytes = kFp8 ? kD : 2 * kD;
   static constexpr int kOperand = kTile * kRowBytes;       // K or V of a tile
   static constexpr int kStage = 2 * kOperand;
   static constexpr int kScales = kFp8 ? 2 * kTile * 4 : 0;  // its scales, K then V
-  static constexpr int kSlots = kFp8 ? (kD == 128 ? 36 : 72) : (kD == 128 ? 24 : 48);  // stages of all warps
+  static constexpr int kSlots = kFp8 ? (kD == 128 ? 32 : 64) : (kD == 128 ? 24 : 48);  // stages of all warps
   static constexpr int kJoin = 2 * kD * 8 * 4;              // a team's buffer: two warps' 8 rows
   static constexpr size_t kSmem = 1024 + (size_t)kSlots * (kStage + kScales) + kTeams * kJoin;
-  static_assert(kSmem + 8704 <= 232448, "shared memory of a CTA");
+  static_assert(kSmem + 10240 <= 232448, "shared memory of a CTA");
 };
 
 // An item and the stretch of keys in it that has to be read.
@@ -259,6 +261,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
   __shared__ int first_item[kMaxB + 1];  // items before the i-th sequence of the order
   __shared__ uint16_t order[kMaxB];      // sequences, those with the largest splits first
   __shared__ float red_m[L::kTeams][2][kTeam][kNq], red_l[L::kTeams][2][kTeam][kNq];
+  __shared__ int near_lens[kNear];       // lengths of the first sequences
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* all = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -278,9 +281,10 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
   // the counts until the first loads.)
   int* counts = reinterpret_cast<int*>(all);
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-    const int n = span_of(a, b).n;
+    const int len = a.lens[b], n = span_of(a, len).n;
     counts[b] = n_splits(n) * 128 + split_blocks(n);
-    if (blockIdx.x == 0 && a.lens[b] > a.n_max) raise_err(a.err, CSA_DEV_ERR_RANGE);
+    if (b < kNear) near_lens[b] = len;
+    if (blockIdx.x == 0 && len > a.n_max) raise_err(a.err, CSA_DEV_ERR_RANGE);
   }
   __syncthreads();
   if (warp == 0) {
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
     c.chunk = in_b - x * chunks;
     c.split = a.kv_shift >= 0 ? x >> a.kv_shift : x / a.n_kv;
     c.kvh = x - c.split * a.n_kv;
-    c.s = span_of(a, c.b);
+    c.s = span_of(a, c.b < kNear ? near_lens[c.b] : a.lens[c.b]);
     const int n = split_blocks(c.s.n), b0 = c.s.b0 + c.split * n;
     c.t = max(b0 * kBlock, c.s.lo) / kTile + w4;
     c.t_end = c.s.n == 0 ? 0 : (min((b0 + n) * kBlock, c.s.len) + kTile - 1) / kTile;
@@ -844,7 +848,7 @@ __global__ void __launch_bounds__(256) gqa_join_kernel(const DecodeArgs a) {
   const int row = blockIdx.x, h = blockIdx.y, b = row / a.T, tau = row % a.T;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // (lens was complete before gqa_decode_kernel let this kernel begin)
-  const int n = n_splits(span_of(a, b).n);
+  const int n = n_splits(span_of(a, a.lens[b]).n);
   const float sink = a.sink ? a.sink[h] * kLog2e : -INFINITY;
   pdl_wait();
   if (n == 1) return;  // finished by gqa_decode_kernel
