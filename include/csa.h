@@ -479,7 +479,9 @@ csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
  *   n_max       host upper bound on lens (n_max <= table_cols * page);
  *               a longer sequence is read up to n_max with CSA_DEV_ERR_RANGE
  *   sink        fp32 [n_heads], or NULL for none
- *   ws          workspace of gqa_decode_attn_workspace_bytes(params, T, n_max)
+ *   ws          workspace of gqa_decode_attn_workspace_bytes(params, T, n_max);
+ *               calls that may run at the same time (other streams, graphs)
+ *               need one each
  * T is at most 64.  The keys of a page not in [0, n_pages) are skipped with
  * CSA_DEV_ERR_INDEX.  What masked slots hold (infinities and NaN included)
  * does not matter; logits of seen keys must be finite in fp32.  The

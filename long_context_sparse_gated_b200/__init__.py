@@ -87,6 +87,7 @@ class GqaRows(ctypes.Structure):
 
 
 class GqaCache(ctypes.Structure):
+    layout = None  # (kv heads, page, d, bytes per element) of make_gqa_cache's tensors
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64)]
 
@@ -324,9 +325,39 @@ def make_gqa_cache(k, v, k_scale=None, v_scale=None) -> GqaCache:
     """gqa_cache over device tensors: k and v [n_pages, n_kv_heads, page, d]
     (+ scales [n_pages, n_kv_heads, page] for an FP8 cache).  The tensors
     stay the caller's: keep them alive as long as the handle is used."""
-    if k.shape != v.shape or (k_scale is None) != (v_scale is None):
+    if k.shape != v.shape or k.dtype != v.dtype or (k_scale is None) != (v_scale is None):
         raise ValueError("keys and values are cached alike")
-    return GqaCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0])
+    if k.dim() != 4 or (k_scale is None) != (k.element_size() == 2):
+        raise ValueError("a cache is [n_pages, n_kv_heads, page, d] of 16 bits, or of 8 with scales")
+    for s in (k_scale, v_scale):
+        if s is not None and (s.shape != k.shape[:3] or s.element_size() != 4):
+            raise ValueError("scales are fp32 [n_pages, n_kv_heads, page]")
+    cache = GqaCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0])
+    cache.layout = (k.shape[1], k.shape[2], k.shape[3], k.element_size())
+    return cache
+
+
+def _check_cache(params, cache):
+    if cache.layout is not None and cache.layout != (params.n_kv_heads, params.page, params.d,
+                                                     1 if params.kv_fmt == KV_FP8 else 2):
+        raise ValueError("the cache's tensors are not those that params describes")
+
+
+def _ints(x, shape):
+    """Device pointer of a contiguous int32 CUDA tensor of that shape."""
+    if x.shape != shape:
+        raise ValueError(f"expected {shape}, got {tuple(x.shape)}")
+    if x.element_size() != 4 or x.is_floating_point():
+        raise TypeError(f"expected int32, got {x.dtype}")
+    return _ptr(x)
+
+
+def _sink(x, heads):
+    if x is None:
+        return None
+    if x.shape != (heads,) or x.element_size() != 4 or not x.is_floating_point():
+        raise ValueError(f"sinks are fp32 [{heads}]")
+    return _ptr(x)
 
 
 _NO_ROWS = GqaRows(None, 0, 0)
@@ -378,8 +409,10 @@ def gqa_cache_append(params, q, k, v, cu, pos0, cache, table, q_out=None, k_out=
     rqo = _NO_ROWS if q_out is None else _rows(q_out, ty, n, hq, d)
     rko = _NO_ROWS if k_out is None else _rows(k_out, ty, n, hk, d)
     _on_device(ty)
-    st = lib().gqa_cache_append(ctypes.byref(params), rq, rk, rv, n, _ptr(cu), _ptr(pos0), cache, _ptr(table),
-                                table.shape[1], rqo, rko, _ptr(err), _stream(stream))
+    _check_cache(params, cache)
+    B, cols = params.B, table.shape[1]
+    st = lib().gqa_cache_append(ctypes.byref(params), rq, rk, rv, n, _ints(cu, (B + 1,)), _ints(pos0, (B,)), cache,
+                                _ints(table, (B, cols)), cols, rqo, rko, _ptr(err), _stream(stream))
     if st:
         _check("gqa_cache_append", st)
 
@@ -396,8 +429,10 @@ def gqa_decode_attn(params, q, cache, table, lens, T, n_max, out, ws=None, sink=
     n, hq, d = params.B * T, params.n_heads, params.d
     rq, ro = _rows(q, ty, n, hq, d), _rows(out, ty, n, hq, d)
     _on_device(ty)
-    st = lib().gqa_decode_attn(ctypes.byref(params), rq, cache, _ptr(table), table.shape[1], _ptr(lens), T, n_max,
-                               _ptr(sink), ro, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(err),
+    _check_cache(params, cache)
+    cols = table.shape[1]
+    st = lib().gqa_decode_attn(ctypes.byref(params), rq, cache, _ints(table, (params.B, cols)), cols,
+                               _ints(lens, (params.B,)), T, n_max, _sink(sink, hq), ro, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(err),
                                _stream(stream))
     if st:
         _check("gqa_decode_attn", st)
@@ -412,7 +447,7 @@ def gqa_prompt_attn(params, q, k, v, cu_q, cu_k, out, sink=None, err=None, strea
     n, m, hk, hq, d = q.shape[0], k.shape[0], params.n_kv_heads, params.n_heads, params.d
     rq, rk, rv, ro = _rows(q, ty, n, hq, d), _rows(k, ty, m, hk, d), _rows(v, ty, m, hk, d), _rows(out, ty, n, hq, d)
     _on_device(ty)
-    st = lib().gqa_prompt_attn(ctypes.byref(params), rq, rk, rv, n, m, _ptr(cu_q), _ptr(cu_k), _ptr(sink), ro, _ptr(err),
-                               _stream(stream))
+    st = lib().gqa_prompt_attn(ctypes.byref(params), rq, rk, rv, n, m, _ints(cu_q, (params.B + 1,)),
+                               _ints(cu_k, (params.B + 1,)), _sink(sink, hq), ro, _ptr(err), _stream(stream))
     if st:
         _check("gqa_prompt_attn", st)

@@ -344,13 +344,13 @@ csa_status gqa_cache_append(const gqa_params* p, gqa_rows q, gqa_rows k, gqa_row
   if (p->r < 0 || p->r > p->d || (p->r & 7)) return CSA_ERR_UNSUPPORTED;
   if (!(p->rope_theta > 0.f)) return CSA_ERR_INVALID;
   if (!cu || !pos0 || n_tokens < 0 || !q.ptr != !q_out.ptr) return CSA_ERR_INVALID;
-  if (n_tokens > INT32_MAX) return CSA_ERR_UNSUPPORTED;
+  if (n_tokens > INT32_MAX / 2) return CSA_ERR_UNSUPPORTED;
   if (!aligned16(cu) || !aligned16(pos0)) return CSA_ERR_ALIGN;
   if ((s = check_gqa_cache(p, cache, table, table_cols)) != CSA_OK) return s;
+  if (n_tokens == 0) return CSA_OK;
   if (q.ptr && ((s = check_rows(p, q)) != CSA_OK || (s = check_rows(p, q_out)) != CSA_OK)) return s;
   if ((s = check_rows(p, k)) != CSA_OK || (s = check_rows(p, v)) != CSA_OK) return s;
   if (k_out.ptr && (s = check_rows(p, k_out)) != CSA_OK) return s;
-  if (n_tokens == 0) return CSA_OK;
   return launched(csa::launch_gqa_append(*p, q, k, v, n_tokens, cu, pos0, cache, table, table_cols, q_out, k_out, err,
                                          reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -371,6 +371,7 @@ csa_status gqa_decode_attn(const gqa_params* p, gqa_rows q, gqa_cache cache, con
   if (n_max > table_cols * p->page) return CSA_ERR_INVALID;
   if ((s = check_rows(p, q)) != CSA_OK || (s = check_rows(p, out)) != CSA_OK) return s;
   if (!aligned16(lens) || (sink && !aligned16(sink))) return CSA_ERR_ALIGN;
+  if (csa::gqa_decode_items(*p, T, n_max) > INT32_MAX) return CSA_ERR_UNSUPPORTED;
   const size_t need = csa::gqa_decode_workspace_bytes(*p, T, n_max);
   if (ws_bytes < need || (need && !ws)) return CSA_ERR_WORKSPACE;
   if (ws && !aligned16(ws)) return CSA_ERR_ALIGN;

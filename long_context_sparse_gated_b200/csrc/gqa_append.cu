@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const __grid_const
 #pragma unroll
         for (int o = kPieces / 2; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
         if (at >= 0 && kind > 0) {
-          const float scale = am == 0.f ? 1.f : __fdiv_rn(am, kE4M3Max);  // NaN in a row: a NaN scale
+          const float s = __fdiv_rn(am, kE4M3Max);  // NaN in a row: a NaN scale
+          const float scale = s == 0.f ? 1.f : s;   // zeros, and what is zero beside fp32's smallest step
           // a reciprocal beyond fp32 (rows below 2^-117): divide
           const float inv = __frcp_rn(scale);
           const bool tiny = !(inv < INFINITY);

@@ -924,6 +924,9 @@ int most_blocks(const gqa_params& p, int T, int n_max) {
   return (int)((keys + kBlock - 1) / kBlock);
 }
 
+// 8 query rows per item where they hold the whole group, else 16.
+int rows_per_item(const gqa_params& p, int T) { return T * (p.n_heads / p.n_kv_heads) <= 8 ? 8 : 16; }
+
 template <bool kBf16, bool kFp8, int kD, int kNq>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeArgs& a, int64_t items, cudaStream_t st) {
   using L = Layout<kFp8, kD, kNq>;
@@ -937,6 +940,11 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeArg
 }
 
 }  // namespace
+
+int64_t gqa_decode_items(const gqa_params& p, int T, int n_max) {
+  const int rows = T * (p.n_heads / p.n_kv_heads), nq = rows_per_item(p, T);
+  return (int64_t)p.B * most_splits(most_blocks(p, T, n_max)) * p.n_kv_heads * ((rows + nq - 1) / nq);
+}
 
 size_t gqa_decode_workspace_bytes(const gqa_params& p, int T, int n_max) {
   const int s = most_splits(most_blocks(p, T, n_max));
@@ -970,11 +978,9 @@ cudaError_t launch_gqa_decode(const gqa_params& p, const gqa_rows& q, const gqa_
   if ((1 << kv_shift) != p.n_kv_heads) kv_shift = -1;
   const DecodeArgs a{q, out, cache.k_scale, cache.v_scale, table, table_cols, lens, sink, part_o,
                      splits > 1 ? reinterpret_cast<float2*>(part_o + slots * p.d) : nullptr, cache.n_pages, p.B, T,
-                     n_max, p.n_heads, p.n_kv_heads, kv_shift, p.page, shift, p.window, splits, p.softmax_scale * kLog2e, err};
-  // 8 query rows per item where they hold the whole group, else 16
-  const int rows = T * (p.n_heads / p.n_kv_heads), nq = rows <= 8 ? 8 : 16;
-  const int64_t items = (int64_t)p.B * splits * p.n_kv_heads * ((rows + nq - 1) / nq);
-  if (items > INT32_MAX) return cudaErrorInvalidValue;
+                     n_max, p.n_heads, p.n_kv_heads, kv_shift, p.page, shift, p.window < (1 << 30) ? p.window : 0, splits, p.softmax_scale * kLog2e, err};
+  const int nq = rows_per_item(p, T);
+  const int64_t items = gqa_decode_items(p, T, n_max);
 #define GQA_GO(BF, F8)                                                                                              \
   (p.d == 128 ? (nq == 8 ? launch<BF, F8, 128, 8>(mk, mv, a, items, st) : launch<BF, F8, 128, 16>(mk, mv, a, items, st)) \
               : (nq == 8 ? launch<BF, F8, 64, 8>(mk, mv, a, items, st) : launch<BF, F8, 64, 16>(mk, mv, a, items, st)))

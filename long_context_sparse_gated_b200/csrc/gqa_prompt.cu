@@ -82,6 +82,7 @@ struct __align__(1024) PromptSmem {
   uint64_t s_full[2], p_full[2][2], o_full;  // p_full: of a unit's half tile
   uint32_t tmem;
   int abort;
+  int blocks[kThreads / 32];  // of a warp's sequences
   int item[6];  // sequence (-1: none), its block, first query, queries, first key, keys
 };
 
@@ -257,64 +258,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   // ---- which sequence, pair of units and KV head
   const int G = a.n_heads / a.n_kv;
-  if (warp == 0) {
-    int base = 0, found = -1, rest = 0;
-    for (int b0 = 0; b0 < a.B && found < 0; b0 += 32) {
-      int n = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-      if (b0 + lane < a.B) {
-        q0 = a.cu_q[b0 + lane];
-        q1 = a.cu_q[b0 + lane + 1];
-        k0 = a.cu_k[b0 + lane];
-        k1 = a.cu_k[b0 + lane + 1];
-        if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k) {
-          if (blockIdx.x == 0) raise_err(a.err, CSA_DEV_ERR_RANGE);
-        } else {
-          n = ((q1 - q0 + kTile - 1) / kTile * G + 1) / 2 * a.n_kv;
-        }
+  if (threadIdx.x == 0) {
+    S.item[0] = -1;
+    S.abort = 0;
+    sm100::mbar_init(&S.q_full, 1);
+    for (int i = 0; i < Smem::kK; ++i) {
+      sm100::mbar_init(&S.k_full[i], 1);
+      sm100::mbar_init(&S.k_empty[i], 1);
+    }
+    for (int i = 0; i < Smem::kV; ++i) {
+      sm100::mbar_init(&S.v_full[i], 1);
+      sm100::mbar_init(&S.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&S.s_full[i], 1);
+      for (int x = 0; x < 2; ++x) sm100::mbar_init(&S.p_full[i][x], 4);
+    }
+    sm100::mbar_init(&S.o_full, 1);
+    sm100::fence_mbar_init();
+  }
+  // a sequence per thread, kThreads of them at a time
+  for (int b0 = 0, base = 0; b0 < a.B; b0 += kThreads) {
+    int n = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+    const int b = b0 + threadIdx.x;
+    if (b < a.B) {
+      q0 = a.cu_q[b];
+      q1 = a.cu_q[b + 1];
+      k0 = a.cu_k[b];
+      k1 = a.cu_k[b + 1];
+      if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k) {
+        raise_err(a.err, CSA_DEV_ERR_RANGE);
+      } else {
+        n = ((q1 - q0 + kTile - 1) / kTile * G + 1) / 2 * a.n_kv;
       }
-      int x = n;
+    }
+    int x = n;
 #pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const int at = (int)blockIdx.x - base - (x - n);
-      const unsigned hit = __ballot_sync(0xffffffffu, at >= 0 && at < n);
-      if (hit) {
-        found = b0 + __ffs(hit) - 1;
-        const int src = __ffs(hit) - 1;
-        rest = __shfl_sync(0xffffffffu, at, src);
-        const int w0 = __shfl_sync(0xffffffffu, q0, src), w1 = __shfl_sync(0xffffffffu, q1, src);
-        const int w2 = __shfl_sync(0xffffffffu, k0, src), w3 = __shfl_sync(0xffffffffu, k1, src);
-        if (lane == 0) {
-          S.item[2] = w0;
-          S.item[3] = w1 - w0;
-          S.item[4] = w2;
-          S.item[5] = w3 - w2;
-        }
-      }
-      base += __shfl_sync(0xffffffffu, x, 31);
+    for (int o = 1; o < 32; o *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    if (lane == 0) {
-      S.item[0] = found;
-      S.item[1] = rest;
-      S.abort = 0;
-      sm100::mbar_init(&S.q_full, 1);
-      for (int i = 0; i < Smem::kK; ++i) {
-        sm100::mbar_init(&S.k_full[i], 1);
-        sm100::mbar_init(&S.k_empty[i], 1);
-      }
-      for (int i = 0; i < Smem::kV; ++i) {
-        sm100::mbar_init(&S.v_full[i], 1);
-        sm100::mbar_init(&S.v_empty[i], 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        sm100::mbar_init(&S.s_full[i], 1);
-        for (int x = 0; x < 2; ++x) sm100::mbar_init(&S.p_full[i][x], 4);
-      }
-      sm100::mbar_init(&S.o_full, 1);
-      sm100::fence_mbar_init();
+    if (b0 > 0) __syncthreads();  // the last sums are read
+    if (lane == 31) S.blocks[warp] = x;
+    __syncthreads();
+    int before = base;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      base += S.blocks[w];
+      if (w < warp) before += S.blocks[w];
     }
+    const int at = (int)blockIdx.x - before - (x - n);
+    if (at >= 0 && at < n) {
+      S.item[0] = b;
+      S.item[1] = at;
+      S.item[2] = q0;
+      S.item[3] = q1 - q0;
+      S.item[4] = k0;
+      S.item[5] = k1 - k0;
+    }
+    if ((int)blockIdx.x < base) break;  // (the same for all threads)
   }
   __syncthreads();
   sm100::tc_fence_after();
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_col = tmem + 128 * i + lanes, o_col = tmem + 256 + kD * i + lanes;
     const int t = u.t0 + r;
     float m = -INFINITY, l = 0.f;  // m in units of S
-    const float step = kLazy / a.scale;
+    const float step = fminf(kLazy / a.scale, 3.0e38f);
     for (int n = 0; n < work; ++n) {
       const int key0 = (u.j0 + n) * kTile;
       float s[128];
@@ -684,8 +685,8 @@ cudaError_t launch_gqa_prompt(const gqa_params& p, const gqa_rows& q, const gqa_
   if (!encode(&mq, q, n_q, p.n_heads) || !encode(&mk, n_k ? k : q, n_k ? n_k : n_q, n_k ? p.n_kv_heads : p.n_heads) ||
       !encode(&mv, n_k ? v : q, n_k ? n_k : n_q, n_k ? p.n_kv_heads : p.n_heads))
     return cudaErrorInvalidValue;
-  const PromptArgs a{q, k, v, out, (int)n_q, (int)n_k, cu_q, cu_k, sink,
-                     p.B, p.n_heads, p.n_kv_heads, p.window, p.softmax_scale * kLog2e, err};
+  const PromptArgs a{q, k, v, out, (int)n_q, (int)n_k, cu_q, cu_k, sink, p.B, p.n_heads, p.n_kv_heads,
+                     p.window < (1 << 30) ? p.window : 0, p.softmax_scale * kLog2e, err};
   // the most pairs of units that B sequences of n_q queries can have
   const int64_t G = p.n_heads / p.n_kv_heads, tiles = n_q / kTile + (n_q < p.B ? n_q : p.B);
   const int64_t blocks = (tiles * G + p.B + 1) / 2 * p.n_kv_heads;

@@ -116,6 +116,7 @@ cudaError_t launch_gqa_append(const gqa_params& p, const gqa_rows& q, const gqa_
                               int32_t* err, cudaStream_t st);
 
 size_t gqa_decode_workspace_bytes(const gqa_params& p, int T, int n_max);
+int64_t gqa_decode_items(const gqa_params& p, int T, int n_max);  // the most work items of a call
 cudaError_t launch_gqa_decode(const gqa_params& p, const gqa_rows& q, const gqa_cache& cache, const int32_t* table,
                               int64_t table_cols, const int32_t* lens, int T, int n_max, const float* sink,
                               const gqa_rows& out, void* ws, int32_t* err, cudaStream_t st);

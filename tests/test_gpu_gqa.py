@@ -617,3 +617,125 @@ def test_decode_many_passes_over_a_large_cache(lib, kv):
         want = torch.softmax(z, -1) @ vv
         # weights of tens of thousands of keys, each off by 2^-8 at most
         assert (outs[0][b].float().view(G, H // G, d) - want).abs().max() < 2.0 ** -8 * (want.abs().max() + vv.abs().mean())
+
+
+# ---- the ends of the ranges ----------------------------------------------------
+
+def test_decode_more_than_64k_keys(lib):
+    """Sequences on both sides of the length where splits grow again, one of
+    them with a window."""
+    lens, G, H, d, page = [66000, 65536, 65537, 3], 1, 4, 64, 256
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cols = -(-max(lens) // page)
+    k, v = (torch.randn((4 * cols, G, page, d), generator=g, device="cuda").half() for _ in range(2))
+    table = torch.randperm(4 * cols, generator=g, device="cuda").int().view(4, cols)
+    q = torch.randn((4, H, d), generator=g, device="cuda").half()
+    for window in (0, 65600):
+        p = _params(lib, "f16", B=4, n_heads=H, n_kv_heads=G, d=d, page=page, softmax_scale=0.2, window=window)
+        ws = torch.empty(lib.gqa_decode_attn_workspace_bytes(p, 1, 66000), dtype=torch.uint8, device="cuda")
+        out, err = torch.empty_like(q), _err()
+        lib.gqa_decode_attn(p, q, lib.make_gqa_cache(k, v), table, _i32(lens), 1, 66000, out, ws, err=err)
+        assert int(err[0]) == 0
+        for b, n in enumerate(lens):
+            kk, vv = (x[table[b].long()].transpose(1, 2).reshape(-1, G, d)[:n] for x in (k, v))
+            want, mag, zmag = gqa.attend(f64(q[b:b + 1]), f64(kk), f64(vv), [n - 1], 0.2, window)
+            check_out(out[b:b + 1], want, mag, zmag, "f16", f"{n} keys, window {window}")
+
+
+def test_a_thousand_sequences(lib):
+    """B at its limit, lengths of 0 to 40, through all three calls."""
+    B, H, G, d, page = 1024, 4, 2, 64, 16
+    rng = np.random.RandomState(3)
+    lens = rng.randint(0, 41, B)
+    lens[[0, 500, 1023]] = [0, 40, 1]
+    n = int(lens.sum())
+    p = _params(lib, B=B, n_heads=H, n_kv_heads=G, d=d, r=d, page=page, softmax_scale=0.2)
+    q, k, v = _randn((n, H, d), "bf16", 1).cuda(), _randn((n, G, d), "bf16", 2).cuda(), _randn((n, G, d), "bf16", 3).cuda()
+    cols = 3
+    table = torch.from_numpy(rng.permutation(B * cols).reshape(B, cols).astype(np.int32)).cuda()
+    kc, vc = (torch.zeros(B * cols, G, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cu, err, ko, qo = _starts(lens), _err(), torch.empty_like(k), torch.empty_like(q)
+    lib.gqa_cache_append(p, q, k, v, cu, _i32([0] * B), lib.make_gqa_cache(kc, vc), table, q_out=qo, k_out=ko, err=err)
+    out = torch.empty_like(q)
+    lib.gqa_prompt_attn(p, qo, ko, v, cu, cu, out, err=err)
+    # each sequence's last query again, from the cache
+    last = torch.from_numpy(np.maximum(np.cumsum(lens) - 1, 0)).cuda()
+    dq = qo[last].contiguous()
+    do = torch.empty_like(dq)
+    ws = torch.empty(max(16, lib.gqa_decode_attn_workspace_bytes(p, 1, 40)), dtype=torch.uint8, device="cuda")
+    lib.gqa_decode_attn(p, dq, lib.make_gqa_cache(kc, vc), table, _i32(list(lens)), 1, 40, do, ws, err=err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    check_turned(ko, gqa.rotate(f64(k), np.concatenate([np.arange(m) for m in lens]), d, THETA), k, "bf16")
+    for b, m in enumerate(lens):
+        a = starts[b]
+        want, mag, zmag = gqa.attend(f64(qo[a:a + m]), f64(ko[a:a + m]), f64(v[a:a + m]), np.arange(m), 0.2)
+        check_out(out[a:a + m], want, mag, zmag, "bf16", f"prompt {b}")
+        if m:
+            check_out(do[b:b + 1], want[-1:], mag[-1:], zmag, "bf16", f"token {b}")
+        else:
+            assert (do[b] == 0).all()
+
+
+def test_nothing_to_do(lib):
+    """No tokens, no keys, an empty batch of lengths: outputs are zeros or left
+    alone."""
+    p = _params(lib, B=2, n_heads=4, n_kv_heads=2, d=64, r=64, page=16, softmax_scale=0.1)
+    kc = torch.full((2, 2, 16, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    empty, kv = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    zero, table = _i32([0, 0, 0]), _i32([[0], [1]])
+    lib.gqa_cache_append(p, empty, kv, kv, zero, _i32([0, 0]), lib.make_gqa_cache(kc, kc.clone()), table, q_out=empty, k_out=kv)
+    lib.gqa_prompt_attn(p, empty, kv, kv, zero, zero, empty)
+    q = _randn((2, 4, 64), "bf16", 1).cuda()
+    out = torch.full_like(q, 9.0)
+    lib.gqa_prompt_attn(p, q, kv, kv, _i32([0, 1, 2]), zero, out)
+    assert (out == 0).all() and (kc == 3).all()
+    out.fill_(9.0)
+    lib.gqa_decode_attn(p, q, lib.make_gqa_cache(kc, kc.clone()), table, _i32([0, 0]), 1, 0, out,
+                        sink=torch.zeros(4, device="cuda"))
+    assert (out == 0).all()
+
+
+def test_windows_wider_than_any_sequence(lib):
+    for window in ((1 << 30) - 1, 1 << 30, (1 << 31) - 1):
+        _prompt(lib, [200, 5], window=window)
+        _decode(lib, [200, 5, 0], "bf16", "act", 4, 2, 64, 16, T=3, window=window)
+
+
+def test_prompt_bad_sequences_between_good_ones(lib):
+    p = _params(lib, B=5, n_heads=2, n_kv_heads=1, d=64, softmax_scale=0.125)
+    q, k = _randn((60, 2, 64), "bf16", 1).cuda(), _randn((60, 1, 64), "bf16", 2).cuda()
+    out, err = torch.full_like(q, 9.0), _err()
+    # the third runs backwards, the fourth has keys from before the first
+    lib.gqa_prompt_attn(p, q, k, k, _i32([0, 10, 25, 20, 40, 60]), _i32([0, 10, 25, -3, 40, 60]), out, err=err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == lib.DEV_ERR_RANGE
+    for a, b in ((0, 10), (10, 25), (40, 60)):
+        want, mag, zmag = gqa.attend(f64(q[a:b]), f64(k[a:b]), f64(k[a:b]), np.arange(b - a), 0.125)
+        check_out(out[a:b], want, mag, zmag, "bf16")
+    assert (out[25:40] == 9).all()
+
+
+def test_append_rows_near_zero_and_not_finite(lib):
+    """FP8 rows whose scale would be below fp32's smallest step are zeros; a
+    NaN or an infinity shows in the row's scale and reaches who sees the row."""
+    p = _params(lib, "bf16", "fp8", B=1, n_heads=2, n_kv_heads=1, d=64, r=0, page=16, softmax_scale=0.1)
+    k = _randn((5, 1, 64), "bf16", 1).cuda()
+    v = _randn((5, 1, 64), "bf16", 2).cuda()
+    v[1] = 0
+    v[1, 0, 3] = 2.0 ** -133
+    v[3, 0, 7], v[4, 0, 9] = float("nan"), float("inf")
+    kc, vc = (torch.zeros(1, 1, 16, 64, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.zeros(1, 1, 16, device="cuda") for _ in range(2))
+    cache = lib.make_gqa_cache(kc, vc, ks, vs)
+    lib.gqa_cache_append(p, None, k, v, _i32([0, 5]), _i32([0]), cache, _i32([[0]]))
+    s = vs[0, 0, :5].cpu()
+    assert torch.isfinite(s[:3]).all() and (s[:3] > 0).all() and torch.isnan(s[3]) and torch.isinf(s[4])
+    back = vc[0, 0, :3].float().cpu() * s[:3, None]
+    assert torch.isfinite(back).all() and back[1].abs().max() <= 2.0 ** -132
+    q = _randn((3, 2, 64), "bf16", 3).cuda()
+    out = torch.empty_like(q)
+    lib.gqa_decode_attn(p, q, cache, _i32([[0]]), _i32([4]), 3, 16, out,
+                        torch.empty(max(16, lib.gqa_decode_attn_workspace_bytes(p, 3, 16)), dtype=torch.uint8, device="cuda"))
+    assert torch.isfinite(out[:2].float()).all() and torch.isnan(out[2].float()).all()

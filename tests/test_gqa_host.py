@@ -94,3 +94,56 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         lib.gqa_decode_attn(p, x, None, cu[None], cu, 1, 3, torch.empty_like(x))
     with pytest.raises(ValueError):
         lib.make_gqa_cache(kv, kv[:1])
+
+
+class _Cuda(torch.Tensor):
+    """A host tensor that says it is on the current device, for the binding's
+    checks (every call below fails one of them before a pointer is used)."""
+
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def _fake(x):
+    return x.as_subclass(_Cuda)
+
+
+def test_binding_refuses_wrong_types_and_caches(monkeypatch):
+    import long_context_sparse_gated_b200 as lib
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+
+    class Unreached:
+        def __getattr__(self, name):
+            return lambda *a: pytest.fail("a refused call reached the library")
+
+    monkeypatch.setattr(lib, "lib", lambda *a: Unreached())
+    p = lib.make_gqa_params(B=1, n_heads=4, n_kv_heads=2, d=64, page=16)
+    q, kv = _fake(torch.zeros(1, 4, 64).bfloat16()), _fake(torch.zeros(1, 2, 64).bfloat16())
+    pages = _fake(torch.zeros(3, 2, 16, 64).bfloat16())
+    codes, scale = _fake(torch.zeros(3, 2, 16, 64, dtype=torch.uint8)), _fake(torch.zeros(3, 2, 16))
+    table, one, cu = (_fake(torch.zeros(s, dtype=torch.int32)) for s in ((1, 4), (1,), (2,)))
+    cache = lib.make_gqa_cache(pages, pages)
+    decode = lambda c=cache, t=table, n=one, x=q, o=q, **kw: lib.gqa_decode_attn(p, x, c, t, n, 1, 9, o, **kw)
+    for call, what in ((lambda: decode(lib.make_gqa_cache(pages[:, :1], pages[:, :1])), ValueError),   # KV heads
+                       (lambda: decode(lib.make_gqa_cache(codes, codes, scale, scale)), ValueError),     # FP8 for 16 bits
+                       (lambda: decode(lib.make_gqa_cache(pages[:, :, :8], pages[:, :, :8])), (TypeError, ValueError)),
+                       (lambda: decode(t=table.long()), TypeError), (lambda: decode(n=one.float()), TypeError),
+                       (lambda: decode(t=_fake(torch.zeros(2, 4, dtype=torch.int32))), ValueError),
+                       (lambda: decode(n=cu), ValueError), (lambda: decode(x=q.half()), TypeError),
+                       (lambda: decode(sink=_fake(torch.zeros(3))), ValueError),
+                       (lambda: decode(sink=_fake(torch.zeros(4, dtype=torch.float64))), ValueError),
+                       (lambda: decode(o=_fake(torch.zeros(1, 4, 128).bfloat16())[:, :, ::2]), ValueError),
+                       (lambda: lib.gqa_cache_append(p, None, kv, kv, one, one, cache, table), ValueError),
+                       (lambda: lib.gqa_cache_append(p, None, kv, kv, cu, cu, cache, table), ValueError),
+                       (lambda: lib.gqa_prompt_attn(p, q, kv, kv, cu, one, q), ValueError),
+                       (lambda: lib.make_gqa_cache(codes, codes), ValueError),
+                       (lambda: lib.make_gqa_cache(pages, pages, scale, scale), ValueError),
+                       (lambda: lib.make_gqa_cache(codes, codes, scale, scale[:2]), ValueError)):
+        with pytest.raises(what):
+            call()
+    # another device than the current one
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    with pytest.raises(ValueError, match="device"):
+        decode()
