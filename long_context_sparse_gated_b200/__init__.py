@@ -337,63 +337,67 @@ def make_gqa_cache(k, v, k_scale=None, v_scale=None) -> GqaCache:
     return cache
 
 
-def _check_cache(params, cache):
-    if cache.layout is not None and cache.layout != (params.n_kv_heads, params.page, params.d,
-                                                     1 if params.kv_fmt == KV_FP8 else 2):
-        raise ValueError("the cache's tensors are not those that params describes")
+# Checks of the gqa_* calls.  A call takes a dozen of them, so they are made to
+# cost little: torch's names are looked up once, and an argument that passes
+# goes through one comparison each of device, type, shape and strides.
+_torch = _BF16 = _F16 = _FP32 = _INT32 = None
 
 
-def _ints(x, shape):
-    """Device pointer of a contiguous int32 CUDA tensor of that shape."""
-    if x.shape != shape:
-        raise ValueError(f"expected {shape}, got {tuple(x.shape)}")
-    if x.element_size() != 4 or x.is_floating_point():
-        raise TypeError(f"expected int32, got {x.dtype}")
-    return _ptr(x)
+def _torch_names():
+    global _torch, _BF16, _F16, _FP32, _INT32
+    import torch
+    _torch, _BF16, _F16, _FP32, _INT32 = torch, torch.bfloat16, torch.float16, torch.float32, torch.int32
 
 
-def _sink(x, heads):
-    if x is None:
-        return None
-    if x.shape != (heads,) or x.element_size() != 4 or not x.is_floating_point():
-        raise ValueError(f"sinks are fp32 [{heads}]")
-    return _ptr(x)
+def _refuse(x, dtype, device, shape):
+    if tuple(x.shape) != shape:
+        raise ValueError(f"expected {list(shape)}, got {list(x.shape)}")
+    if dtype is _FP32 and x.dtype is not dtype:
+        raise ValueError(f"sinks are fp32, got {x.dtype}")
+    if x.dtype is not dtype:
+        raise TypeError(f"expected {dtype}, got {x.dtype}")
+    if not x.is_cuda:
+        raise TypeError("libcsa takes CUDA tensors (device pointers); got a host array")
+    if x.get_device() != device:
+        raise ValueError(f"tensor on device {x.get_device()}, but device {device} is current")
+    raise ValueError("libcsa takes C-contiguous tensors (rows of heads: contiguous in their last dim)")
+
+
+def _flat(x, dtype, device, shape):
+    """Device pointer of a contiguous tensor of that type, device and shape."""
+    if x.dtype is not dtype or x.get_device() != device or x.shape != shape or not x.is_contiguous():
+        _refuse(x, dtype, device, shape)
+    return x.data_ptr()
 
 
 _NO_ROWS = GqaRows(None, 0, 0)
 
 
-def _gqa_types(params, x):
-    """(torch dtype of act_fmt, current device) that every row tensor has to
-    match: kernels are launched on the current device.  Device -1 if x is a
-    host tensor (refused by _on_device once shapes are checked)."""
-    import torch
-    return (torch.bfloat16 if params.act_fmt == ACT_BF16 else torch.float16,
-            torch._C._cuda_getDevice() if x.is_cuda else -1)
-
-
-def _on_device(types):
-    if types[1] < 0:
-        raise TypeError("libcsa takes CUDA tensors (device pointers); got a host array")
-
-
-def _rows(x, types, n, heads, d):
-    """gqa_rows of a CUDA tensor [n, heads, d] of the activation type; only
-    its last dim has to be contiguous."""
-    dtype, device = types
-    if x.get_device() != device:
-        if not x.is_cuda:
-            _on_device((dtype, -1))
-        raise ValueError(f"tensor on device {x.get_device()}, but device {device} is current")
-    if x.dtype is not dtype:
-        raise TypeError(f"act_fmt says {dtype}, got {x.dtype}")
-    if x.shape != (n, heads, d):
-        raise ValueError(f"expected [{n}, {heads}, {d}], got {tuple(x.shape)}")
-    sn, sh, sd = x.stride()
-    if sd != 1:
-        raise ValueError("the last dim of a row tensor has to be contiguous")
+def _rows(x, dtype, device, n, heads, d):
+    """gqa_rows of a tensor [n, heads, d]; only its last dim has to be
+    contiguous."""
+    sn, sh, sd = x.stride() if x.dim() == 3 else (0, 0, 0)
+    if x.dtype is not dtype or x.get_device() != device or sd != 1 or x.shape != (n, heads, d):
+        _refuse(x, dtype, device, (n, heads, d))
     # the stride of a single row or head is never used
     return GqaRows(x.data_ptr(), sn if n > 1 else max(sn, d), sh if heads > 1 else max(sh, d))
+
+
+def _gqa_call(params):
+    """The type that rows have, and the current device, on which kernels are
+    launched and every tensor has to be."""
+    if _torch is None:
+        _torch_names()
+    try:
+        device = _torch._C._cuda_getDevice()
+    except RuntimeError:
+        device = None  # no device: every tensor is refused as a host tensor
+    return _BF16 if params.act_fmt == ACT_BF16 else _F16, device
+
+
+def _check_cache(params, cache, heads, d):
+    if cache.layout is not None and cache.layout != (heads, params.page, d, 1 if params.kv_fmt == KV_FP8 else 2):
+        raise ValueError("the cache's tensors are not those that params describes")
 
 
 def gqa_cache_append(params, q, k, v, cu, pos0, cache, table, q_out=None, k_out=None, err=None, stream=None):
@@ -402,17 +406,17 @@ def gqa_cache_append(params, q, k, v, cu, pos0, cache, table, q_out=None, k_out=
     ``cache`` through ``table`` ([B, cols]), keys turned by their positions.
     Turned queries (``q`` [n, n_heads, d], or None) go to ``q_out``, turned
     keys to ``k_out`` (both may be the inputs)."""
-    n, d, hk, hq = k.shape[0], params.d, params.n_kv_heads, params.n_heads
-    ty = _gqa_types(params, k)
-    rk, rv = _rows(k, ty, n, hk, d), _rows(v, ty, n, hk, d)
-    rq = _NO_ROWS if q is None else _rows(q, ty, n, hq, d)
-    rqo = _NO_ROWS if q_out is None else _rows(q_out, ty, n, hq, d)
-    rko = _NO_ROWS if k_out is None else _rows(k_out, ty, n, hk, d)
-    _on_device(ty)
-    _check_cache(params, cache)
-    B, cols = params.B, table.shape[1]
-    st = lib().gqa_cache_append(ctypes.byref(params), rq, rk, rv, n, _ints(cu, (B + 1,)), _ints(pos0, (B,)), cache,
-                                _ints(table, (B, cols)), cols, rqo, rko, _ptr(err), _stream(stream))
+    n, d, hk, hq, B = k.shape[0], params.d, params.n_kv_heads, params.n_heads, params.B
+    ty, dev = _gqa_call(params)
+    rq = _NO_ROWS if q is None else _rows(q, ty, dev, n, hq, d)
+    rk, rv = _rows(k, ty, dev, n, hk, d), _rows(v, ty, dev, n, hk, d)
+    rqo = _NO_ROWS if q_out is None else _rows(q_out, ty, dev, n, hq, d)
+    rko = _NO_ROWS if k_out is None else _rows(k_out, ty, dev, n, hk, d)
+    _check_cache(params, cache, hk, d)
+    cols = table.shape[-1]
+    st = lib().gqa_cache_append(ctypes.byref(params), rq, rk, rv, n, _flat(cu, _INT32, dev, (B + 1,)),
+                                _flat(pos0, _INT32, dev, (B,)), cache, _flat(table, _INT32, dev, (B, cols)), cols, rqo, rko,
+                                None if err is None else _ptr(err), _stream(stream))
     if st:
         _check("gqa_cache_append", st)
 
@@ -425,15 +429,15 @@ def gqa_decode_attn(params, q, cache, table, lens, T, n_max, out, ws=None, sink=
     """The last T tokens of every sequence (``q``, ``out`` [B*T, n_heads, d])
     attend to the lens[b] <= n_max cached keys of their sequence; ``ws`` is a
     CUDA byte tensor of gqa_decode_attn_workspace_bytes(params, T, n_max)."""
-    ty = _gqa_types(params, q)
-    n, hq, d = params.B * T, params.n_heads, params.d
-    rq, ro = _rows(q, ty, n, hq, d), _rows(out, ty, n, hq, d)
-    _on_device(ty)
-    _check_cache(params, cache)
-    cols = table.shape[1]
-    st = lib().gqa_decode_attn(ctypes.byref(params), rq, cache, _ints(table, (params.B, cols)), cols,
-                               _ints(lens, (params.B,)), T, n_max, _sink(sink, hq), ro, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(err),
-                               _stream(stream))
+    B, hq, d = params.B, params.n_heads, params.d
+    ty, dev = _gqa_call(params)
+    rq, ro = _rows(q, ty, dev, B * T, hq, d), _rows(out, ty, dev, B * T, hq, d)
+    _check_cache(params, cache, params.n_kv_heads, d)
+    cols = table.shape[-1]
+    st = lib().gqa_decode_attn(ctypes.byref(params), rq, cache, _flat(table, _INT32, dev, (B, cols)), cols,
+                               _flat(lens, _INT32, dev, (B,)), T, n_max, None if sink is None else _flat(sink, _FP32, dev, (hq,)),
+                               ro, None if ws is None else _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                               None if err is None else _ptr(err), _stream(stream))
     if st:
         _check("gqa_decode_attn", st)
 
@@ -443,11 +447,12 @@ def gqa_prompt_attn(params, q, k, v, cu_q, cu_k, out, sink=None, err=None, strea
     cu_q[b]..cu_q[b+1]-1 of ``q`` and ``out`` ([n_q, n_heads, d]), its keys
     and values rows cu_k[b]..cu_k[b+1]-1 of ``k`` and ``v`` ([n_k,
     n_kv_heads, d]); the last query sits at the last key."""
-    ty = _gqa_types(params, q)
-    n, m, hk, hq, d = q.shape[0], k.shape[0], params.n_kv_heads, params.n_heads, params.d
-    rq, rk, rv, ro = _rows(q, ty, n, hq, d), _rows(k, ty, m, hk, d), _rows(v, ty, m, hk, d), _rows(out, ty, n, hq, d)
-    _on_device(ty)
-    st = lib().gqa_prompt_attn(ctypes.byref(params), rq, rk, rv, n, m, _ints(cu_q, (params.B + 1,)),
-                               _ints(cu_k, (params.B + 1,)), _sink(sink, hq), ro, _ptr(err), _stream(stream))
+    n, m, B, hk, hq, d = q.shape[0], k.shape[0], params.B, params.n_kv_heads, params.n_heads, params.d
+    ty, dev = _gqa_call(params)
+    rv, rk = _rows(v, ty, dev, m, hk, d), _rows(k, ty, dev, m, hk, d)
+    rq, ro = _rows(q, ty, dev, n, hq, d), _rows(out, ty, dev, n, hq, d)
+    st = lib().gqa_prompt_attn(ctypes.byref(params), rq, rk, rv, n, m, _flat(cu_q, _INT32, dev, (B + 1,)),
+                               _flat(cu_k, _INT32, dev, (B + 1,)), None if sink is None else _flat(sink, _FP32, dev, (hq,)), ro,
+                               None if err is None else _ptr(err), _stream(stream))
     if st:
         _check("gqa_prompt_attn", st)
