@@ -4,6 +4,10 @@ The five calls keep the C ABI's names (see include/csa.h):
 
     csa_compress, hca_compress, csa_index_topk, csa_sparse_attn, hca_dense_attn
 
+and so do the three of grouped-query attention over a paged cache:
+
+    gqa_cache_append, gqa_decode_attn, gqa_prompt_attn
+
 This module only marshals arguments: it turns CUDA tensors into device
 pointers and a torch stream into a cudaStream_t, and raises on a non-OK
 status.  Every step of the computation runs in the library's kernels.  There
