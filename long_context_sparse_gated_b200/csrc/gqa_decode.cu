@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
   __syncthreads();
   if (warp == 0) {
     int items = 0, place = 0;
+#pragma unroll 1
     for (int c = kMaxSplit; c >= kMinSplit; c /= 2)
       for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int x = b0 + lane < a.B ? counts[b0 + lane] : 0;
@@ -768,45 +769,62 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
           f[e] = v != 0.f ? 1.f / v : 0.f;
         }
       }
-      // Pieces of rows: a lane takes column 2 q4 + (g & 1) of itself and its
-      // neighbour lane ^ 4 (16-bit cache: two dims from 16 mt + 8 e2 + (g & 6)),
-      // or both columns, four dims each (FP8 cache: from kD/8 g + 4 j).
-      auto put = [&](int col, int dim, const float* x, int n) {
-        const int r = c.chunk * kNq + 8 * nt + col;
-        if (r >= rows) return;
-        const int tau = r / G, h = c.kvh * G + r - tau * G;
-        if (single) {
-          uint16_t* dst = reinterpret_cast<uint16_t*>(a.out.ptr) + ((int64_t)c.b * a.T + tau) * a.out.row_stride +
-                          (int64_t)h * a.out.head_stride + dim;
-          if (n == 2) *reinterpret_cast<uint32_t*>(dst) = pack2<kBf16>(x[0], x[1]);
-          else *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<kBf16>(x[0], x[1]), pack2<kBf16>(x[2], x[3]));
-        } else {
-          const int64_t slot = (((int64_t)c.b * a.max_splits + c.split) * a.T + tau) * a.n_heads + h;
-          float* dst = a.part_o + slot * kD + dim;
-          if (n == 2) *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[1]);
-          else *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+      // Pieces of rows.  16-bit cache: a lane takes column 2 q4 + (g & 1) of itself
+      // and its neighbour lane ^ 4, two dims from 16 mt + 8 e2 + (g & 6); FP8 cache:
+      // both its columns, four dims each from kD/8 g + 4 j.
+      int64_t at[2] = {-1, -1};  // of the columns' rows: in the output, or in the partial results
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = c.chunk * kNq + 8 * nt + 2 * q4 + (kFp8 ? e : g & 1);
+        if (r < rows) {
+          const int tau = r / G, h = c.kvh * G + r - tau * G;
+          at[e] = single ? ((int64_t)c.b * a.T + tau) * a.out.row_stride + (int64_t)h * a.out.head_stride
+                         : ((((int64_t)c.b * a.max_splits + c.split) * a.T + tau) * a.n_heads + h) * kD;
         }
-      };
+        if (!kFp8) break;
+      }
       if (!kFp8) {
         const bool hi = g & 1;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(a.out.ptr) + at[0] + (g & 6);
+        float* part = a.part_o + at[0] + (g & 6);
 #pragma unroll
         for (int mt = 0; mt < kD / 16; ++mt)
 #pragma unroll
           for (int e2 = 0; e2 < 2; ++e2) {
             const float x0 = o[mt][nt][2 * e2] * f[0], x1 = o[mt][nt][2 * e2 + 1] * f[1];
             const float y = __shfl_xor_sync(0xffffffffu, hi ? x0 : x1, 4);
-            const float x[2] = {hi ? y : x0, hi ? x1 : y};
-            put(2 * q4 + hi, 16 * mt + 8 * e2 + (g & 6), x, 2);
+            o[mt][nt][2 * e2] = hi ? y : x0;
+            o[mt][nt][2 * e2 + 1] = hi ? x1 : y;
           }
+        if (at[0] >= 0) {
+          if (single) {
+#pragma unroll
+            for (int mt = 0; mt < kD / 16; ++mt)
+#pragma unroll
+              for (int e2 = 0; e2 < 2; ++e2)
+                *reinterpret_cast<uint32_t*>(dst + 16 * mt + 8 * e2) = pack2<kBf16>(o[mt][nt][2 * e2], o[mt][nt][2 * e2 + 1]);
+          } else {
+#pragma unroll
+            for (int mt = 0; mt < kD / 16; ++mt)
+#pragma unroll
+              for (int e2 = 0; e2 < 2; ++e2)
+                *reinterpret_cast<float2*>(part + 16 * mt + 8 * e2) = make_float2(o[mt][nt][2 * e2], o[mt][nt][2 * e2 + 1]);
+          }
+        }
       } else {
 #pragma unroll
-        for (int j = 0; j < kD / 32; ++j)
+        for (int e = 0; e < 2; ++e) {
+          if (at[e] < 0) continue;
+          uint16_t* dst = reinterpret_cast<uint16_t*>(a.out.ptr) + at[e] + kD / 8 * g;
+          float* part = a.part_o + at[e] + kD / 8 * g;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x[4] = {o[2 * j][nt][e] * f[e], o[2 * j][nt][2 + e] * f[e], o[2 * j + 1][nt][e] * f[e],
-                                o[2 * j + 1][nt][2 + e] * f[e]};
-            put(2 * q4 + e, kD / 8 * g + 4 * j, x, 4);
+          for (int j = 0; j < kD / 32; ++j) {
+            const float4 x = make_float4(o[2 * j][nt][e] * f[e], o[2 * j][nt][2 + e] * f[e], o[2 * j + 1][nt][e] * f[e],
+                                         o[2 * j + 1][nt][2 + e] * f[e]);
+            if (single) *reinterpret_cast<uint2*>(dst + 4 * j) = make_uint2(pack2<kBf16>(x.x, x.y), pack2<kBf16>(x.z, x.w));
+            else *reinterpret_cast<float4*>(part + 4 * j) = x;
           }
+        }
       }
       if (!single && g == 0) {
 #pragma unroll

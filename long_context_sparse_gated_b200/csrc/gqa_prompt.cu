@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= alpha;
         if (n > 0) {
           // S being here says that the products before it are done
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < kD; c += 16) {
             uint32_t w[16];
             sm100::tmem_ld_x16(o_col + c, w);
@@ -606,7 +606,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t top = 0;  // largest magnitude of the row, as bits
       constexpr int kChunks = kD / 8;  // 16-byte pieces of a row
       uint4* stage = reinterpret_cast<uint4*>(S.q[i]) + (warp & 3) * 32 * kChunks;  // the warp's 32 rows
-#pragma unroll
+      // (rolled: it runs once, and instructions that are fetched for the first
+      // time cost more than the loop)
+#pragma unroll 1
       for (int c = 0; c < kD; c += 16) {
         uint32_t w[16];
         if (work > 0) {
@@ -630,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (!*abort) {
-#pragma unroll
+#pragma unroll 4
         for (int x = lane; x < 32 * kChunks; x += 32) {
           const int row = x / kChunks, ch = x % kChunks;
           if ((warp & 3) * 32 + row < u.rows) {
