@@ -9,6 +9,20 @@
 namespace csa {
 namespace gqa {
 
+// 2^x and 1/x to about an fp32 step, inline.  (The precise division is a
+// subroutine: the first call in a launch fetches it, which took the prompt
+// kernel's softmax 5000 clocks.)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Two packed 16-bit activations <-> fp32 (kBf16: BF16, else FP16).
 template <bool kBf16>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {

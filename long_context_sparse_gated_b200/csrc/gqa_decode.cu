@@ -127,11 +127,6 @@ __device__ __forceinline__ Span span_of(const DecodeArgs& a, int len) {
   return s;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -766,7 +761,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
           const int r = c.chunk * kNq + 8 * nt + 2 * q4 + e;
           float v = l[nt][e];
           if (a.sink && r < rows && m[nt][e] != -INFINITY) v += ex2(a.sink[c.kvh * G + r % G] * kLog2e - m[nt][e]);
-          f[e] = v != 0.f ? 1.f / v : 0.f;
+          f[e] = v != 0.f ? rcp(v) : 0.f;
         }
       }
       // Pieces of rows.  16-bit cache: a lane takes column 2 q4 + (g & 1) of itself
@@ -929,7 +924,7 @@ __global__ void __launch_bounds__(256) gqa_join_kernel(const DecodeArgs a) {
       l = fmaf(red_l[w], f, l);
     }
     if (top != -INFINITY) l += ex2(sink - top);
-    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? rcp(l) : 0.f;
     uint16_t* dst = reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)row * a.out.row_stride +
                     (int64_t)h * a.out.head_stride + 2 * threadIdx.x;
     *reinterpret_cast<uint32_t*>(dst) = pack2<kBf16>(x * inv, y * inv);

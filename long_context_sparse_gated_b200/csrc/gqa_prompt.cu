@@ -44,6 +44,8 @@
 // Rounding: P to the activation type (relative 2^-9 or 2^-12); the rest fp32.
 #include <cuda.h>
 
+#include <cmath>
+
 #include "gqa.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -67,7 +69,7 @@ struct PromptArgs {
   const int32_t* cu_k;
   const float* sink;
   int B, n_heads, n_kv, window;
-  float scale;  // softmax_scale * log2(e)
+  float scale, step;  // softmax_scale * log2(e); kLazy in units of S
   int32_t* err;
 };
 
@@ -86,11 +88,6 @@ struct __align__(1024) PromptSmem {
   int item[6];  // sequence (-1: none), its block, first query, queries, first key, keys
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float (&r)[128], int at) {
   uint32_t* u = reinterpret_cast<uint32_t*>(r) + at;
@@ -233,7 +230,7 @@ __device__ __noinline__ void one_row(const PromptArgs& a, const Unit& u, int kvh
     m = mn;
   }
   if (a.sink && m != -INFINITY) l += ex2(a.sink[u.head] * kLog2e - m);
-  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const float inv = l != 0.f ? rcp(l) : 0.f;
 #pragma unroll
   for (int e = 0; e < n; e += 2)
     *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)(u.row0 + r) * a.out.row_stride +
@@ -482,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_col = tmem + 128 * i + lanes, o_col = tmem + 256 + kD * i + lanes;
     const int t = u.t0 + r;
     float m = -INFINITY, l = 0.f;  // m in units of S
-    const float step = fminf(kLazy / a.scale, 3.0e38f);
     for (int n = 0; n < work; ++n) {
       const int key0 = (u.j0 + n) * kTile;
       float s[128];
@@ -534,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const bool over = top > m + step;
+      const bool over = top > m + a.step;
       if (__any_sync(0xffffffffu, over)) {
         const float alpha = over ? ex2((m - top) * a.scale) : 1.f;  // 0 from -inf
         if (over) m = top;
@@ -602,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (u.rows > 0) {
       if (a.sink && m != -INFINITY) l += ex2(a.sink[u.head] * kLog2e - m * a.scale);
-      const float f = l != 0.f ? 1.f / l : 0.f;
+      const float f = l != 0.f ? rcp(l) : 0.f;
       uint32_t top = 0;  // largest magnitude of the row, as bits
       constexpr int kChunks = kD / 8;  // 16-byte pieces of a row
       uint4* stage = reinterpret_cast<uint4*>(S.q[i]) + (warp & 3) * 32 * kChunks;  // the warp's 32 rows
@@ -687,8 +683,9 @@ cudaError_t launch_gqa_prompt(const gqa_params& p, const gqa_rows& q, const gqa_
   if (!encode(&mq, q, n_q, p.n_heads) || !encode(&mk, n_k ? k : q, n_k ? n_k : n_q, n_k ? p.n_kv_heads : p.n_heads) ||
       !encode(&mv, n_k ? v : q, n_k ? n_k : n_q, n_k ? p.n_kv_heads : p.n_heads))
     return cudaErrorInvalidValue;
+  const float scale = p.softmax_scale * kLog2e;
   const PromptArgs a{q, k, v, out, (int)n_q, (int)n_k, cu_q, cu_k, sink, p.B, p.n_heads, p.n_kv_heads,
-                     p.window < (1 << 30) ? p.window : 0, p.softmax_scale * kLog2e, err};
+                     p.window < (1 << 30) ? p.window : 0, scale, fminf(kLazy / scale, 3.0e38f), err};
   // the most pairs of units that B sequences of n_q queries can have
   const int64_t G = p.n_heads / p.n_kv_heads, tiles = n_q / kTile + (n_q < p.B ? n_q : p.B);
   const int64_t blocks = (tiles * G + p.B + 1) / 2 * p.n_kv_heads;
