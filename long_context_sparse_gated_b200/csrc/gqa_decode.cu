@@ -247,7 +247,7 @@ struct Item {
 template <bool kBf16, bool kFp8, int kD, int kNq>
 __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                      const DecodeArgs a) {
+                      const __grid_constant__ DecodeArgs a) {
   using L = Layout<kFp8, kD, kNq>;
   constexpr int kNt = kNq / 8;
   constexpr bool kMmaBf16 = kBf16 && !kFp8;
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
 // split's (m, l) while the outputs are already on their way; the warps'
 // results are then added in order.
 template <bool kBf16, int kD>
-__global__ void __launch_bounds__(256) gqa_join_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(256) gqa_join_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int kV = kD / 32;
   __shared__ float red[8][kD];
   __shared__ float red_l[8], red_m[8];

@@ -199,10 +199,10 @@ struct Unit {
   int j0, j1;      // key tiles [j0, j1)
 };
 
-// Row r of a unit on its own, by a warp: the path for rows that came out as
-// something not finite.
+// One row (packed query row `row`, at position t) on its own, by a warp: the
+// path for rows that came out as something not finite.
 template <bool kBf16, int kD>
-__device__ __noinline__ void one_row(const PromptArgs& a, const Unit& u, int kvh, int k0, int r, int lane) {
+__device__ __noinline__ void one_row(const PromptArgs& a, int row, int t, int head, int kvh, int k0, int lane) {
   constexpr int n = kD / 32;
   auto load = [&](const gqa_rows& s, int64_t row, int h, float (&x)[n]) {
 #pragma unroll
@@ -213,9 +213,9 @@ __device__ __noinline__ void one_row(const PromptArgs& a, const Unit& u, int kvh
       x[j + 1] = f.y;
     }
   };
-  const int t = u.t0 + r, first = a.window > 0 ? max(0, t - a.window + 1) : 0;
+  const int first = a.window > 0 ? max(0, t - a.window + 1) : 0;
   float q[n], x[n], o[n] = {}, m = -INFINITY, l = 0.f;
-  load(a.q, u.row0 + r, u.head, q);
+  load(a.q, row, head, q);
   for (int j = first; j <= t; ++j) {
     load(a.k, k0 + j, kvh, x);
     float z = 0.f;
@@ -229,18 +229,18 @@ __device__ __noinline__ void one_row(const PromptArgs& a, const Unit& u, int kvh
     for (int e = 0; e < n; ++e) o[e] = fmaf(p, x[e], f == 0.f ? 0.f : o[e] * f);
     m = mn;
   }
-  if (a.sink && m != -INFINITY) l += ex2(a.sink[u.head] * kLog2e - m);
+  if (a.sink && m != -INFINITY) l += ex2(a.sink[head] * kLog2e - m);
   const float inv = l != 0.f ? rcp(l) : 0.f;
 #pragma unroll
   for (int e = 0; e < n; e += 2)
-    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)(u.row0 + r) * a.out.row_stride +
-                                 u.head * a.out.head_stride + n * lane + e) = pack2<kBf16>(o[e] * inv, o[e + 1] * inv);
+    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)row * a.out.row_stride +
+                                 head * a.out.head_stride + n * lane + e) = pack2<kBf16>(o[e] * inv, o[e + 1] * inv);
 }
 
 template <bool kBf16, int kD>
 __global__ void __launch_bounds__(kThreads, 1)
     gqa_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                      const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PromptArgs a) {
   using Smem = PromptSmem<kD>;
   extern __shared__ uint8_t raw[];
   Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- loads
       int n_live = (work0 > 0) + (work1 > 0);
       if (n_live) sm100::mbar_arrive_expect_tx(&S.q_full, n_live * Smem::kOperand);
+#pragma unroll
       for (int i = 0; i < 2; ++i)
         if ((i ? work1 : work0) > 0)
           for (int c = 0; c < kD / 64; ++c)
@@ -639,7 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         for (unsigned odd = __ballot_sync(0xffffffffu, r < u.rows && top >= 0x7F800000u); odd; odd &= odd - 1)
-          one_row<kBf16, kD>(a, u, kvh, k_begin, (warp & 3) * 32 + __ffs(odd) - 1, lane);
+          {
+          const int x = (warp & 3) * 32 + __ffs(odd) - 1;
+          one_row<kBf16, kD>(a, u.row0 + x, u.t0 + x, u.head, kvh, k_begin, lane);
+        }
       }
     }
   }
