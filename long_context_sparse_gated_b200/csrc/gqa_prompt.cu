@@ -26,11 +26,13 @@
 //
 // Exponentials.  A tile pair has 32768 of them: 2048 clocks of the 16-lane
 // special-function pipe, as many as its four products take.  So kPoly of
-// every 8 pairs of logits go through the FMA pipe instead: 2^x = 2^n 2^f with n
-// the nearest integer (by adding 1.5 * 2^23) and a polynomial of degree 4 in f
-// (minimax for the relative error on [-1/2, 1/2]: 2.6e-6), n added to the
-// exponent field; weights below 2^-126 of the row's largest come out as about
-// that.  Packed fp32 pairs (f32x2) throughout.
+// every 8 pairs of logits (3 for BF16, 2 for FP16; 16K tokens take 417 us with
+// 3, 425 with 2, 446 with 1, 474 with none) go through the FMA pipe instead: 2^x =
+// 2^n 2^f with n the nearest integer (by adding 1.5 * 2^23) and a polynomial in f,
+// minimax for the relative error on [-1/2, 1/2]: degree 3, 7.5e-5, before P is
+// rounded to BF16 (2^-9), degree 4, 2.6e-6, before FP16 (2^-12).  n is added to
+// the exponent field; weights below 2^-126 of the row's largest come out as
+// about that.  Packed fp32 pairs (f32x2) throughout.
 //
 // Masks.  In tiles that some row does not see as a whole logits are selected,
 // blocks of 32 keys that a warp's rows all see or all miss at once.  A value
@@ -60,7 +62,6 @@ constexpr int kTile = 128;  // query positions of a unit, keys of a tile
 constexpr int kThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;  // base-2 units
-constexpr int kPoly = 2;      // of 8 pairs of exponentials, on the FMA pipe
 
 struct PromptArgs {
   gqa_rows q, k, v, out;
@@ -165,6 +166,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 // 2^x of two numbers that are at most 127 (smaller ones than -126 count as -126).
+template <bool kBf16>
 __device__ __forceinline__ uint64_t exp2_poly(uint64_t x2) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
   float x, y;
@@ -172,10 +174,17 @@ __device__ __forceinline__ uint64_t exp2_poly(uint64_t x2) {
   x2 = f32x2(fmaxf(x, -126.f), fmaxf(y, -126.f));
   const uint64_t t2 = add2(x2, f32x2(kMagic, kMagic));  // the low bits hold round(x)
   const uint64_t f2 = fma2(add2(t2, f32x2(-kMagic, -kMagic)), f32x2(-1.f, -1.f), x2);
-  uint64_t p2 = fma2(f2, f32x2(0.009570102207362652f, 0.009570102207362652f), f32x2(0.05591785907745361f, 0.05591785907745361f));
-  p2 = fma2(f2, p2, f32x2(0.240247443318367f, 0.240247443318367f));
-  p2 = fma2(f2, p2, f32x2(0.6931217908859253f, 0.6931217908859253f));
-  p2 = fma2(f2, p2, f32x2(0.9999992847442627f, 0.9999992847442627f));
+  uint64_t p2;
+  if (kBf16) {
+    p2 = fma2(f2, f32x2(0.0551716685295105f, 0.0551716685295105f), f32x2(0.2426111251115799f, 0.2426111251115799f));
+    p2 = fma2(f2, p2, f32x2(0.6932609677314758f, 0.6932609677314758f));
+    p2 = fma2(f2, p2, f32x2(0.9999280571937561f, 0.9999280571937561f));
+  } else {
+    p2 = fma2(f2, f32x2(0.009570102207362652f, 0.009570102207362652f), f32x2(0.05591785907745361f, 0.05591785907745361f));
+    p2 = fma2(f2, p2, f32x2(0.240247443318367f, 0.240247443318367f));
+    p2 = fma2(f2, p2, f32x2(0.6931217908859253f, 0.6931217908859253f));
+    p2 = fma2(f2, p2, f32x2(0.9999992847442627f, 0.9999992847442627f));
+  }
   float tx, ty;
   split2(t2, tx, ty);
   split2(p2, x, y);
@@ -475,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- softmax: unit i, row r
     const int i = warp >> 2, r = (warp & 3) * 32 + lane;
     const Unit u = i ? un[1] : un[0];
+    constexpr int kPoly = kBf16 ? 3 : 2;
     const int work = i ? work1 : work0;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + 128 * i + lanes, o_col = tmem + 256 + kD * i + lanes;
@@ -566,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t x2 = fma2(f32x2(s[64 * half + 2 * c], s[64 * half + 2 * c + 1]), scale2, mc2);
             float x, y;
             if (decltype(poly)::value && (c * kPoly) % 8 < kPoly) {
-              const uint64_t y2 = exp2_poly(x2);
+              const uint64_t y2 = exp2_poly<kBf16>(x2);
               split2(y2, x, y);
               sum2[c & 1] = add2(sum2[c & 1], y2);
             } else {
