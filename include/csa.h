@@ -458,7 +458,7 @@ typedef struct gqa_cache {
  * The turn is computed in fp32 (angles reduced in fp64).  CSA_KV_ACT rounds
  * the result once; CSA_KV_FP8 stores scale = amax/448 over the row's d values
  * (1 for a row of zeros) and the E4M3 codes of value / scale, both from the
- * fp32 result (the quotient within an fp32 rounding or two); a row that holds a NaN or an infinity gets that as its scale.  A token whose position is negative or past the table raises
+ * fp32 result (quotients within an fp32 rounding or two); a row that holds a NaN or an infinity gets that as its scale.  A token whose position is negative or past the table raises
  * CSA_DEV_ERR_RANGE, one whose page is not in [0, n_pages) CSA_DEV_ERR_INDEX;
  * it is not stored (q_out and k_out are written all the same).  Two tokens
  * of one call must not share a cache slot. */

@@ -13,9 +13,10 @@
 // host in fp64, the product is reduced to [-1/2, 1/2] turns in fp64 and only
 // then rounded, so that an angle is off by 2^-25 turns at any position.
 //
-// FP8.  The lanes that hold a row agree on its largest magnitude; codes are
-// those of value * (1 / scale), which differs from value / scale by an fp32
-// rounding (a code differs only where the quotient is that near a border).
+// FP8.  The lanes that hold a row agree on its largest magnitude.  The scale
+// is amax * (1/448) and codes are those of value * (1 / scale): both differ from
+// the quotients by an fp32 rounding or two (a code only where the quotient is
+// that near a border), and there is no division subroutine to fetch.
 #include <cmath>
 #include <cstring>
 
@@ -199,10 +200,10 @@ __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const __grid_const
 #pragma unroll
         for (int o = kPieces / 2; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
         if (at >= 0 && kind > 0) {
-          const float s = __fdiv_rn(am, kE4M3Max);  // NaN in a row: a NaN scale
+          const float s = am * (1.f / kE4M3Max);    // NaN in a row: a NaN scale
           const float scale = s == 0.f ? 1.f : s;   // zeros, and what is zero beside fp32's smallest step
           // a reciprocal beyond fp32 (rows below 2^-117): divide
-          const float inv = __frcp_rn(scale);
+          const float inv = rcp(scale);
           const bool tiny = !(inv < INFINITY);
           uint32_t u[8];
 #pragma unroll
