@@ -75,7 +75,7 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int B, int i, int lan
 }
 
 template <bool kBf16, bool kFp8, int kD>
-__global__ void __launch_bounds__(kThreads) gqa_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, kFp8 ? 4 : 5) gqa_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kPieces = kD / 16;  // of a row: 8 or 4 neighbouring lanes
   __shared__ __align__(16) float2 turn[kMaxTokens][kD / 2];
   __shared__ int64_t row0[kMaxTokens];  // page * n_kv * page size + slot, -1: not stored, -2: no token

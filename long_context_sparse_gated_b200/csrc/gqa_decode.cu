@@ -29,18 +29,17 @@
 // 16-bit cache.  m16n8k16; K by ldmatrix, V by ldmatrix.trans, P^T rounded to
 // 16 bits and transposed in registers by movmatrix.
 //
-// FP8 cache.  E4M3 codes become FP16 in registers (m16n8k32 on 8-bit operands
-// is no way around it: here it compiles to conversions and m16n8k16), K's by
-// the conversion instruction, which goes through the 16-lane special-function
-// pipe, V's by moving bits, three or four ALU instructions for two codes.
-// One pipe alone takes 278 or 208 us for 24 sequences of up to 32K keys.  The
-// dims of a 16-byte piece are dealt to MMA steps in an order that Q's
-// fragments share, so no shuffles are needed.  A query row is brought into
-// FP16 by a power of two of its own (largest magnitude in [2^14, 2^15); what is
-// 2^29 below that loses bits that do not show in fp32).  The value's scale s_j
-// joins the weight: w_j = exp2(z_j + log2 s_j - M) with M the running maximum of
-// that sum, so weights stay in (0, 2^8] whatever the scales are, and the
-// denominator sums w_j / s_j.  Value scales are read as within 2^-90 .. 2^90.
+// FP8 cache.  E4M3 codes become FP16 in registers by the packed conversion
+// instruction (moving the bits by hand takes 163 us instead of 129 for 24
+// sequences of up to 32K keys; m16n8k32 on 8-bit operands is no way around it:
+// here it compiles to conversions and m16n8k16).  The dims of a 16-byte piece
+// are dealt to MMA steps in an order that Q's fragments share, so no shuffles
+// are needed.  A query row is brought into FP16 by a power of two of its own
+// (largest magnitude in [2^14, 2^15); what is 2^29 below that loses bits that do
+// not show in fp32).  The value's scale s_j joins the weight: w_j = exp2(z_j +
+// log2 s_j - M) with M the running maximum of that sum, so weights stay in (0,
+// 2^8] whatever the scales are, and the denominator sums w_j / s_j.  Value
+// scales are read as within 2^-90 .. 2^90.
 //
 // Rounding.  Weights are rounded to 16 bits (relative 2^-9 for a BF16 cache,
 // 2^-12 for FP16 and FP8 caches), sums and partial outputs are fp32.
@@ -191,24 +190,12 @@ __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// Two E4M3 codes (low 16 bits) -> two FP16.
-__device__ __forceinline__ uint32_t cvt_codes(uint32_t v) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four E4M3 codes -> FP16, bytes 0, 1 and 2, 3.
+__device__ __forceinline__ void cvt_codes(uint32_t v, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(v));
 }
-// E4M3 codes in bytes 1 and 3 (bytes 0 and 2) -> two FP16 of 2^-8 their
-// value: sign, four exponent and three mantissa bits move to FP16's places
-// (its exponent bias is 8 larger), subnormals included.  `mag` is their
-// magnitude: the NaN codes come out as 0x3F80 (+-480 / 2^8).
-__device__ __forceinline__ uint32_t move_codes13(uint32_t v, uint32_t& mag) {
-  mag = (v >> 1) & 0x3F803F80u;
-  return (v & 0x80008000u) | mag;
-}
-__device__ __forceinline__ uint32_t move_codes02(uint32_t v, uint32_t& mag) { return move_codes13(v << 8, mag); }
-__device__ __forceinline__ bool has_nan_code(uint32_t top) {
-  return (top & 0xFFFFu) == 0x3F80u || (top >> 16) == 0x3F80u;
-}
-constexpr float kCodeExp = 8.f;  // of the moved codes
 
 // Halves of a register that are infinities or NaN, as a mask over them.
 template <bool kBf16>
@@ -223,8 +210,8 @@ constexpr int kMaxB = 1024, kNear = 256;
 template <bool kFp8, int kD, int kNq>
 struct Layout {
   // 8 query rows: three teams of up to 168 registers a thread, or four of 128 for
-  // an FP8 cache, whose work is in the instructions (184 us with three, 167 with
-  // four, 218 with two); 16 rows: two of up to 255
+  // an FP8 cache, whose work is in the instructions (142 us with three, 128 with
+  // four); 16 rows: two of up to 255
   static constexpr int kTeams = kNq == 8 ? (kFp8 ? 4 : 3) : 2, kWarps = kTeam * kTeams;
   static constexpr int kRowBytes = kFp8 ? kD : 2 * kD;
   static constexpr int kOperand = kTile * kRowBytes;       // K or V of a tile
@@ -525,15 +512,16 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
             const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
             for (int sp = 0; sp < 4; ++sp) {
-              const uint32_t af[4] = {cvt_codes(w0[sp]), cvt_codes(w1[sp]), cvt_codes(w0[sp] >> 16), cvt_codes(w1[sp] >> 16)};
+              uint32_t af[4];
+              cvt_codes(w0[sp], af[0], af[2]);
+              cvt_codes(w1[sp], af[1], af[3]);
 #pragma unroll
               for (int nt = 0; nt < kNt; ++nt)
                 mma16816<false>((sp & 1) ? z2[nt] : z[nt], af, qf[nt][8 * i + 2 * sp], qf[nt][8 * i + 2 * sp + 1]);
             }
           }
         }
-        // of keys g, g + 8: K scale, log2 of the V scale (V's codes come as 2^-8
-        // of their value) and 2^ of its negative
+        // of keys g, g + 8: K scale, log2 of the V scale and 2^ of its negative
         float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f}, rv[2] = {1.f, 1.f};
         if (kFp8) {
           const float* sc = scales + st * 2 * kTile + g;
@@ -541,7 +529,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
           for (int e = 0; e < 2; ++e) {
             ks[e] = sc[8 * e];
             const float x = sc[kTile + 8 * e];
-            lv[e] = x != x ? x : fminf(fmaxf(lg2(x), kMinLogScale), kMaxLogScale) + kCodeExp;
+            lv[e] = x != x ? x : fminf(fmaxf(lg2(x), kMinLogScale), kMaxLogScale);
             rv[e] = ex2(-lv[e]);
           }
         }
@@ -622,7 +610,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
         } else {
           // kD/8 codes of keys 2 q4, 2 q4 + 1, + 8, + 9 from dim kD/8 * g on: rows
           // g and g + 8 of m-tile mt are dims 2 mt and 2 mt + 1 of that piece
-          uint32_t w[4][kD / 32], top = 0;
+          uint32_t w[4][kD / 32];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = 2 * q4 + (e & 1) + 8 * (e >> 1);
@@ -640,18 +628,24 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
           }
 #pragma unroll
           for (int mt = 0; mt < kD / 16; ++mt) {
-            const uint32_t sel = (mt & 1) ? 0x7632u : 0x5410u;
-            const uint32_t lo = __byte_perm(w[0][mt / 2], w[1][mt / 2], sel), hi = __byte_perm(w[2][mt / 2], w[3][mt / 2], sel);
-            uint32_t mag[4];
-            const uint32_t af[4] = {move_codes02(lo, mag[0]), move_codes13(lo, mag[1]), move_codes02(hi, mag[2]),
-                                    move_codes13(hi, mag[3])};
-            top = __vimax3_u16x2(__vimax3_u16x2(top, mag[0], mag[1]), mag[2], mag[3]);
+            // dims 2 mt, 2 mt + 1 of the piece, of two keys each
+            const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
+            uint32_t af[4];
+            cvt_codes(__byte_perm(w[0][mt / 2], w[1][mt / 2], sel), af[0], af[1]);
+            cvt_codes(__byte_perm(w[2][mt / 2], w[3][mt / 2], sel), af[2], af[3]);
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t bad = odd_halves<false>(af[e]);
+                odd |= bad != 0;
+                af[e] &= ~bad;
+              }
+            }
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt) mma16816<false>(o[mt][nt], af, pf[nt][0], pf[nt][1]);
           }
-          odd = has_nan_code(top);
         }
-        if (__any_sync(0xffffffffu, odd)) {
+        if (edge && __any_sync(0xffffffffu, odd)) {
           // give each value that is not finite to the rows that see it
 #pragma unroll
           for (int mt = 0; mt < kD / 16; ++mt)
