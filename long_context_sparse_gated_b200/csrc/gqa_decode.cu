@@ -73,10 +73,10 @@ constexpr float kMinLogScale = -90.f, kMaxLogScale = 90.f;
 
 // Blocks per split for a sequence of n blocks: 8, 16 or 32 blocks, so that
 // there are about 12 splits (256 to 1024 keys), and 64 for more than 64K keys.
-// Measured (single 777 keys / 32 mixed up to 16K / 4 of 128K / 24 FP8 up to
-// 32K / 16 x 4 drafted tokens, us): this 14.1 / 153 / 327 / 177 / 16; 4 to 16 blocks
-// and 32 splits 13.8 / 165 / 357 / 201 / 20; up to 32 blocks throughout - / 153 / 346 /
-// 177 / 16; from 16 blocks on 16.4 / 152 / 328 / 179 / 17.
+// Measured (32 mixed up to 16K / 4 of 128K / 24 FP8 up to 32K / 16 x 4 drafted
+// tokens, us): this 151 / 326 / 128 / 15; 4 to 16 blocks and 32 splits 160 / 360 /
+// 140 / 18; never 64 blocks 151 / 339 / 128 / 15; 4 blocks at least 155 / 326 / 128 /
+// 18; 16 at least 147 / 326 / 127 / 15, but 16.4 instead of 14.1 for 777 keys alone.
 constexpr int kMinSplit = 8, kMidSplit = 32, kMaxSplit = 64, kSplits = 12, kLong = 2048;
 __host__ __device__ inline int split_blocks(int n) {
   if (n > kLong) return kMaxSplit;
