@@ -13,6 +13,13 @@
  *                                window + attention sink, inverse RoPE
  *   hca_dense_attn               the same attention over every entry
  *
+ * and, for layers that keep raw keys and values:
+ *
+ *   gqa_cache_append             new keys and values into a paged cache
+ *   gqa_decode_attn              grouped-query attention of the last tokens
+ *                                over that cache
+ *   gqa_prompt_attn              the same, causal, over packed prompts
+ *
  * Sources, by page title and section:
  *   [kwkr]    kwkr.cn DeepSeek-V4 notes, 3.1 CSA 的工作方式, 3.2 HCA 的工作方式,
  *             3.3 层间排布与滑窗补充, 3.4 两个降开销的设计, 4.4 FP4 QAT 与 KV Cache 层级
@@ -458,10 +465,13 @@ typedef struct gqa_cache {
  * The turn is computed in fp32 (angles reduced in fp64).  CSA_KV_ACT rounds
  * the result once; CSA_KV_FP8 stores scale = amax/448 over the row's d values
  * (1 for a row of zeros) and the E4M3 codes of value / scale, both from the
- * fp32 result (quotients within an fp32 rounding or two); a row that holds a NaN or an infinity gets that as its scale.  A token whose position is negative or past the table raises
- * CSA_DEV_ERR_RANGE, one whose page is not in [0, n_pages) CSA_DEV_ERR_INDEX;
+ * fp32 result (quotients within an fp32 rounding or two); a row that holds a
+ * NaN or an infinity gets that as its scale.  A token whose position is
+ * negative or past the table raises CSA_DEV_ERR_RANGE, one whose page is not
+ * in [0, n_pages) CSA_DEV_ERR_INDEX;
  * it is not stored (q_out and k_out are written all the same).  Two tokens
- * of one call must not share a cache slot. */
+ * of one call must not share a cache slot, and beyond q_out = q and k_out = k
+ * (same strides; v is not k then) nothing that is written overlaps an input. */
 csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
                             gqa_rows v, int64_t n_tokens, const int32_t* cu,
                             const int32_t* pos0, gqa_cache cache,
@@ -474,7 +484,7 @@ csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
  * keys at max(0, t-window+1) .. t:
  *   z_j = softmax_scale * q.k_j,  p_j = exp(z_j) / (exp(sink[h]) + sum exp(z_j))
  *   o   = sum_j p_j v_j, written in act_fmt; zeros where no key is seen
- *   q, out      [B*T][n_heads]
+ *   q, out      [B*T][n_heads]; out overlaps no input
  *   lens        int32 [B]: keys in the cache, the new tokens included
  *   n_max       host upper bound on lens (n_max <= table_cols * page);
  *               a longer sequence is read up to n_max with CSA_DEV_ERR_RANGE
@@ -484,8 +494,8 @@ csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
  *               need one each
  * T is at most 64.  The keys of a page not in [0, n_pages) are skipped with
  * CSA_DEV_ERR_INDEX.  What masked slots hold (infinities and NaN included)
- * does not matter; logits of seen keys must be finite in fp32.  The
- * scale of an FP8 value counts as no less than 2^-90 and no more than 2^90.  How a
+ * does not matter; logits of seen keys must be finite in fp32.  The scale of
+ * an FP8 value counts as no less than 2^-90 and no more than 2^90.  How a
  * sequence's keys are split depends on its own length, T and the window
  * alone, and partial results are joined in a fixed order: a query's output
  * is bit-identical run to run and whatever batch it is in. */
@@ -503,7 +513,7 @@ size_t gqa_decode_attn_workspace_bytes(const gqa_params* params, int32_t T,
  * query i of n sits at t = (keys - n) + i and sees the keys at
  * max(0, t-window+1) .. t (none where t < 0: its output is zeros).
  * Softmax, sink and output as in gqa_decode_attn.
- *   q, out      [n_q][n_heads]
+ *   q, out      [n_q][n_heads]; out overlaps no input
  *   k, v        [n_k][n_kv_heads]
  *   cu_q, cu_k  int32 [B+1], not decreasing, first 0, last <= n_q / n_k; output
  *               rows from cu_q[B] on are left as they are

@@ -92,6 +92,7 @@ class GqaRows(ctypes.Structure):
 
 class GqaCache(ctypes.Structure):
     layout = None  # (kv heads, page, d, bytes per element) of make_gqa_cache's tensors
+    dtype = device = None  # and their type and device
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64)]
 
@@ -334,10 +335,15 @@ def make_gqa_cache(k, v, k_scale=None, v_scale=None) -> GqaCache:
     if k.dim() != 4 or (k_scale is None) != (k.element_size() == 2):
         raise ValueError("a cache is [n_pages, n_kv_heads, page, d] of 16 bits, or of 8 with scales")
     for s in (k_scale, v_scale):
-        if s is not None and (s.shape != k.shape[:3] or s.element_size() != 4):
+        if s is not None and (s.shape != k.shape[:3] or str(s.dtype) != "torch.float32"):
             raise ValueError("scales are fp32 [n_pages, n_kv_heads, page]")
+    if k_scale is not None and k.dtype.is_floating_point and str(k.dtype) != "torch.float8_e4m3fn":
+        raise ValueError(f"8-bit caches hold E4M3 codes, got {k.dtype}")
+    if any(s is not None and s.device != k.device for s in (v, k_scale, v_scale)):
+        raise ValueError("a cache's tensors are on one device")
     cache = GqaCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0])
     cache.layout = (k.shape[1], k.shape[2], k.shape[3], k.element_size())
+    cache.dtype, cache.device = k.dtype, k.get_device()
     return cache
 
 
@@ -399,9 +405,26 @@ def _gqa_call(params):
     return _BF16 if params.act_fmt == ACT_BF16 else _F16, device
 
 
-def _check_cache(params, cache, heads, d):
-    if cache.layout is not None and cache.layout != (heads, params.page, d, 1 if params.kv_fmt == KV_FP8 else 2):
+def _check_cache(params, cache, heads, d, ty, device):
+    if cache.layout is None:  # a handle over the caller's own pointers
+        return
+    fp8 = params.kv_fmt == KV_FP8
+    if cache.layout != (heads, params.page, d, 1 if fp8 else 2):
         raise ValueError("the cache's tensors are not those that params describes")
+    if not fp8 and cache.dtype is not ty and cache.dtype.is_floating_point:
+        raise TypeError(f"expected a cache of {ty}, got {cache.dtype}")
+    if cache.device != device:
+        raise ValueError(f"cache on device {cache.device}, but device {device} is current")
+
+
+def _here(x, device):
+    """Device pointer of a workspace or error word, or None."""
+    if x is None:
+        return None
+    ptr = _ptr(x)
+    if not isinstance(x, int) and x.get_device() != device:
+        raise ValueError(f"tensor on device {x.get_device()}, but device {device} is current")
+    return ptr
 
 
 def gqa_cache_append(params, q, k, v, cu, pos0, cache, table, q_out=None, k_out=None, err=None, stream=None):
@@ -416,11 +439,11 @@ def gqa_cache_append(params, q, k, v, cu, pos0, cache, table, q_out=None, k_out=
     rk, rv = _rows(k, ty, dev, n, hk, d), _rows(v, ty, dev, n, hk, d)
     rqo = _NO_ROWS if q_out is None else _rows(q_out, ty, dev, n, hq, d)
     rko = _NO_ROWS if k_out is None else _rows(k_out, ty, dev, n, hk, d)
-    _check_cache(params, cache, hk, d)
+    _check_cache(params, cache, hk, d, ty, dev)
     cols = table.shape[-1]
     st = lib().gqa_cache_append(ctypes.byref(params), rq, rk, rv, n, _flat(cu, _INT32, dev, (B + 1,)),
                                 _flat(pos0, _INT32, dev, (B,)), cache, _flat(table, _INT32, dev, (B, cols)), cols, rqo, rko,
-                                None if err is None else _ptr(err), _stream(stream))
+                                _here(err, dev), _stream(stream))
     if st:
         _check("gqa_cache_append", st)
 
@@ -436,12 +459,12 @@ def gqa_decode_attn(params, q, cache, table, lens, T, n_max, out, ws=None, sink=
     B, hq, d = params.B, params.n_heads, params.d
     ty, dev = _gqa_call(params)
     rq, ro = _rows(q, ty, dev, B * T, hq, d), _rows(out, ty, dev, B * T, hq, d)
-    _check_cache(params, cache, params.n_kv_heads, d)
+    _check_cache(params, cache, params.n_kv_heads, d, ty, dev)
     cols = table.shape[-1]
     st = lib().gqa_decode_attn(ctypes.byref(params), rq, cache, _flat(table, _INT32, dev, (B, cols)), cols,
                                _flat(lens, _INT32, dev, (B,)), T, n_max, None if sink is None else _flat(sink, _FP32, dev, (hq,)),
-                               ro, None if ws is None else _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                               None if err is None else _ptr(err), _stream(stream))
+                               ro, _here(ws, dev), 0 if ws is None else ws.numel() * ws.element_size(),
+                               _here(err, dev), _stream(stream))
     if st:
         _check("gqa_decode_attn", st)
 
@@ -457,6 +480,6 @@ def gqa_prompt_attn(params, q, k, v, cu_q, cu_k, out, sink=None, err=None, strea
     rq, ro = _rows(q, ty, dev, n, hq, d), _rows(out, ty, dev, n, hq, d)
     st = lib().gqa_prompt_attn(ctypes.byref(params), rq, rk, rv, n, m, _flat(cu_q, _INT32, dev, (B + 1,)),
                                _flat(cu_k, _INT32, dev, (B + 1,)), None if sink is None else _flat(sink, _FP32, dev, (hq,)), ro,
-                               None if err is None else _ptr(err), _stream(stream))
+                               _here(err, dev), _stream(stream))
     if st:
         _check("gqa_prompt_attn", st)

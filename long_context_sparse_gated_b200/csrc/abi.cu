@@ -309,7 +309,7 @@ static csa_status check_gqa(const gqa_params* p) {
   if (p->B > 1024 || p->n_heads > 128) return CSA_ERR_UNSUPPORTED;
   if (p->d != 64 && p->d != 128) return CSA_ERR_UNSUPPORTED;
   if (p->act_fmt != CSA_ACT_BF16 && p->act_fmt != CSA_ACT_F16) return CSA_ERR_UNSUPPORTED;
-  if (!(p->softmax_scale > 0.f && p->softmax_scale <= 3.0e38f)) return CSA_ERR_INVALID;
+  if (!(p->softmax_scale > 0.f && p->softmax_scale <= 2.0e38f)) return CSA_ERR_INVALID;
   return CSA_OK;
 }
 
@@ -390,6 +390,7 @@ csa_status gqa_prompt_attn(const gqa_params* p, gqa_rows q, gqa_rows k, gqa_rows
   if (n_q == 0) return CSA_OK;
   if ((s = check_rows(p, q)) != CSA_OK || (s = check_rows(p, out)) != CSA_OK) return s;
   if (n_k > 0 && ((s = check_rows(p, k)) != CSA_OK || (s = check_rows(p, v)) != CSA_OK)) return s;
+  if (out.ptr == q.ptr || (n_k > 0 && (out.ptr == k.ptr || out.ptr == v.ptr))) return CSA_ERR_INVALID;
   return launched(csa::launch_gqa_prompt(*p, q, k, v, n_q, n_k, cu_q, cu_k, sink, out, err,
                                          reinterpret_cast<cudaStream_t>(stream)));
 }

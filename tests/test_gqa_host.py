@@ -147,3 +147,55 @@ def test_binding_refuses_wrong_types_and_caches(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
     with pytest.raises(ValueError, match="device"):
         decode()
+
+
+def test_binding_refuses_caches_and_workspaces_of_another_type_or_device(monkeypatch):
+    import long_context_sparse_gated_b200 as lib
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+
+    class Elsewhere(_Cuda):
+        def get_device(self):
+            return 1
+
+    class Unreached:
+        def __getattr__(self, name):
+            return lambda *a: pytest.fail("a refused call reached the library")
+
+    monkeypatch.setattr(lib, "lib", lambda *a: Unreached())
+    p = lib.make_gqa_params(B=1, n_heads=4, n_kv_heads=2, d=64, page=16)
+    q, kv = _fake(torch.zeros(1, 4, 64).bfloat16()), _fake(torch.zeros(1, 2, 64).bfloat16())
+    pages = torch.zeros(3, 2, 16, 64).bfloat16()
+    codes, scale = _fake(torch.zeros(3, 2, 16, 64, dtype=torch.uint8)), _fake(torch.zeros(3, 2, 16))
+    table, one, cu = (_fake(torch.zeros(s, dtype=torch.int32)) for s in ((1, 4), (1,), (2,)))
+    cache = lib.make_gqa_cache(_fake(pages), _fake(pages))
+    half = lib.make_gqa_cache(_fake(pages.half()), _fake(pages.half()))
+    there = lib.make_gqa_cache(pages.as_subclass(Elsewhere), pages.as_subclass(Elsewhere))
+    far = torch.zeros(64, dtype=torch.int32).as_subclass(Elsewhere)
+    decode = lambda c, **kw: lib.gqa_decode_attn(p, q, c, table, one, 1, 9, q, **kw)
+    append = lambda c, **kw: lib.gqa_cache_append(p, None, kv, kv, cu, one, c, table, **kw)
+    for call, what in ((lambda: decode(half), TypeError), (lambda: append(half), TypeError),
+                       (lambda: decode(there), ValueError), (lambda: append(there), ValueError),
+                       (lambda: decode(cache, ws=far), ValueError), (lambda: decode(cache, err=far), ValueError),
+                       (lambda: append(cache, err=far), ValueError),
+                       (lambda: lib.gqa_prompt_attn(p, q, kv, kv, cu, cu, _fake(torch.zeros(1, 4, 64).bfloat16()), err=far), ValueError),
+                       (lambda: lib.make_gqa_cache(codes, codes, scale.int(), scale.int()), ValueError),
+                       (lambda: lib.make_gqa_cache(codes.view(torch.float8_e5m2), codes.view(torch.float8_e5m2), scale, scale), ValueError)):
+        with pytest.raises(what):
+            call()
+
+
+def test_prompt_in_place_is_refused():
+    code = """
+import ctypes, sys
+sys.path.insert(0, ROOT)
+import long_context_sparse_gated_b200 as m
+A, B, C = 0x10000, 0x20000, 0x30000
+rows = lambda at: m.GqaRows(at, 512, 128)
+p = ctypes.byref(m.make_gqa_params(B=1, n_heads=4, n_kv_heads=4, d=128))
+for out in (A, B, C):
+    st = m.lib().gqa_prompt_attn(p, rows(A), rows(B), rows(C), 4, 4, A, A, None, rows(out), None, None)
+    assert st == -1, (hex(out), st)
+""".replace("ROOT", repr(ROOT))
+    env = {**os.environ, "CUDA_VISIBLE_DEVICES": ""}
+    done = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr
