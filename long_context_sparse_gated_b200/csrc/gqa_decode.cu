@@ -220,7 +220,7 @@ struct Layout {
   static constexpr int kSlots = kFp8 ? (kD == 128 ? 32 : 64) : (kD == 128 ? 24 : 48);  // stages of all warps
   static constexpr int kJoin = 2 * kD * 8 * 4;              // a team's buffer: two warps' 8 rows
   static constexpr size_t kSmem = 1024 + (size_t)kSlots * (kStage + kScales) + kTeams * kJoin;
-  static_assert(kSmem + 10240 <= 232448, "shared memory of a CTA");
+  static_assert(kSmem + 8192 + 68 * kTeams * kNq <= 232448, "shared memory of a CTA");
 };
 
 // An item and the stretch of keys in it that has to be read.
@@ -237,12 +237,15 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
                       const __grid_constant__ DecodeArgs a) {
   using L = Layout<kFp8, kD, kNq>;
   constexpr int kNt = kNq / 8;
+  constexpr bool kShared = kNq == 32;  // the queries' fragments in shared memory
+  static_assert(!kShared || kNt == kTeam, "a warp brings one n-tile's");
   constexpr bool kMmaBf16 = kBf16 && !kFp8;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t full_bar[L::kSlots];
   __shared__ int first_item[kMaxB + 1];  // items before the i-th sequence of the order
   __shared__ uint16_t order[kMaxB];      // sequences, those with the largest splits first
   __shared__ float red_m[L::kTeams][2][kTeam][kNq], red_l[L::kTeams][2][kTeam][kNq];
+  __shared__ float red_q[L::kTeams][kShared ? kNq : 1];  // logit factors of the rows
   __shared__ int near_lens[kNear];       // lengths of the first sequences
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
   float* scales = reinterpret_cast<float*>(all + L::kSlots * L::kStage + warp * n_st * L::kScales);
   float4* join = reinterpret_cast<float4*>(all + L::kSlots * (L::kStage + L::kScales) + team * L::kJoin);
   uint64_t* full = full_bar + warp * n_st;
-  const uint32_t ring_u32 = sm100::smem_u32(ring), scales_u32 = sm100::smem_u32(scales), full_u32 = sm100::smem_u32(full);
+  const uint32_t ring_u32 = sm100::smem_u32(ring), scales_u32 = sm100::smem_u32(scales), join_u32 = sm100::smem_u32(join), full_u32 = sm100::smem_u32(full);
   volatile int* abort = &abort_flag;
 
   auto enter = [&](Item& c, int item) {
@@ -398,11 +401,12 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
 
     // query fragments: B operand, column g of n-tile nt is query row
     // chunk * kNq + 8 nt + g = tau * G + head
-    uint32_t qf[kNt][kD / 8];
+    uint32_t qf[kShared ? 1 : kNt][kD / 8];
     float qs[kNt][2];  // logit factor of columns 2 q4, 2 q4 + 1
     int tq[kNt][2];    // their positions (INT_MIN: no row)
 #pragma unroll
-    for (int nt = 0; nt < kNt; ++nt) {
+    for (int x = 0; x < (kShared ? 1 : kNt); ++x) {
+      const int nt = kShared ? w4 : x;
       const int r = c.chunk * kNq + 8 * nt + g;
       const bool live = r < rows;
       const int tau = live ? r / G : 0, h = c.kvh * G + (live ? r % G : 0);
@@ -413,8 +417,8 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
         for (int kk = 0; kk < kD / 16; ++kk)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            qf[nt][2 * kk + e] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 * e + 2 * q4) : 0u;
-        qs[nt][0] = qs[nt][1] = a.scale;
+            qf[x][2 * kk + e] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 * e + 2 * q4) : 0u;
+        if (!kShared) qs[x][0] = qs[x][1] = a.scale;
       } else {
         // this lane's dims: kD/4 consecutive ones from kD/4 * q4 on
         uint4 v[kD / 32];
@@ -439,21 +443,48 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] *= down;
           const uint4 u = pack8<false>(f);
-          qf[nt][4 * i] = u.x;
-          qf[nt][4 * i + 1] = u.y;
-          qf[nt][4 * i + 2] = u.z;
-          qf[nt][4 * i + 3] = u.w;
+          qf[x][4 * i] = u.x;
+          qf[x][4 * i + 1] = u.y;
+          qf[x][4 * i + 2] = u.z;
+          qf[x][4 * i + 3] = u.w;
         }
         // column c's factor sits in lanes 4 c .. 4 c + 3
-        qs[nt][0] = a.scale * __shfl_sync(0xffffffffu, up, 8 * q4);
-        qs[nt][1] = a.scale * __shfl_sync(0xffffffffu, up, 8 * q4 + 4);
+        if (kShared) {
+          if (q4 == 0) red_q[team][kShared ? 8 * nt + g : 0] = a.scale * up;
+        } else {
+          qs[x][0] = a.scale * __shfl_sync(0xffffffffu, up, 8 * q4);
+          qs[x][1] = a.scale * __shfl_sync(0xffffffffu, up, 8 * q4 + 4);
+        }
       }
+    }
+    if (kShared) {
+      sm100::named_bar_sync(1 + team, 32 * kTeam);  // the last item's join has read the place
+#pragma unroll
+      for (int j = 0; j < kD / 32; ++j)
+        reinterpret_cast<uint4*>(join)[(w4 * kD / 32 + j) * 32 + lane] =
+            make_uint4(qf[0][4 * j], qf[0][4 * j + 1], qf[0][4 * j + 2], qf[0][4 * j + 3]);
+      sm100::named_bar_sync(1 + team, 32 * kTeam);
+    }
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        if (kShared) qs[nt][e] = kFp8 ? red_q[team][kShared ? 8 * nt + 2 * q4 + e : 0] : a.scale;
         const int rc = c.chunk * kNq + 8 * nt + 2 * q4 + e;
         tq[nt][e] = rc < rows ? c.s.len - a.T + rc / G : INT32_MIN;
       }
     }
+
+    // the queries' fragments 4 j .. 4 j + 3
+    auto q_at = [&](int nt, int j, uint32_t (&b)[4]) {
+      if (kShared) {
+        const uint4 v = lds128(join_u32 + ((nt * kD / 32 + j) * 32 + lane) * 16);
+        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = qf[kShared ? 0 : nt][4 * j + e];
+      }
+    };
 
     float m[kNt][2], l[kNt][2], o[kD / 16][kNt][4];
 #pragma unroll
@@ -482,8 +513,9 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
 
         auto tile = [&](auto kind) {
         constexpr bool edge = decltype(kind)::value;
-        // S^T = K Q^T (keys g, g + 8), in two chains of MMAs
+        // S^T = K Q^T (keys g, g + 8), in two chains of MMAs or more
         float z[kNt][4], z2[kNt][4];
+        uint32_t qb[kNt][4];
 #pragma unroll
         for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
@@ -492,11 +524,16 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
           const int r = lane & 15;
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk) {
+            if (!(kk & 1)) {
+#pragma unroll
+              for (int nt = 0; nt < kNt; ++nt) q_at(nt, kk / 2, qb[nt]);
+            }
             uint32_t af[4];
             const int ch = 2 * (kk & 3) + (lane >> 4);
             ldsm4(sk + (kk >> 2) * kTile * 128 + r * 128 + ((ch ^ (r & 7)) << 4), af);
 #pragma unroll
-            for (int nt = 0; nt < kNt; ++nt) mma16816<kMmaBf16>((kk & 1) ? z2[nt] : z[nt], af, qf[nt][2 * kk], qf[nt][2 * kk + 1]);
+            for (int nt = 0; nt < kNt; ++nt) 
+              mma16816<kMmaBf16>((kk & 1) && !kShared ? z2[nt] : z[nt], af, qb[nt][2 * (kk & 1)], qb[nt][2 * (kk & 1) + 1]);
           }
         } else {
           // 16 codes of keys g and g + 8 at a time: four MMA steps, whose dims
@@ -512,12 +549,16 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
             const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
             for (int sp = 0; sp < 4; ++sp) {
+              if (!(sp & 1)) {
+#pragma unroll
+                for (int nt = 0; nt < kNt; ++nt) q_at(nt, 2 * i + sp / 2, qb[nt]);
+              }
               uint32_t af[4];
               cvt_codes(w0[sp], af[0], af[2]);
               cvt_codes(w1[sp], af[1], af[3]);
 #pragma unroll
               for (int nt = 0; nt < kNt; ++nt)
-                mma16816<false>((sp & 1) ? z2[nt] : z[nt], af, qf[nt][8 * i + 2 * sp], qf[nt][8 * i + 2 * sp + 1]);
+                mma16816<false>((sp & 1) && !kShared ? z2[nt] : z[nt], af, qb[nt][2 * (sp & 1)], qb[nt][2 * (sp & 1) + 1]);
             }
           }
         }
@@ -540,7 +581,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float& u = z[nt][e];
-            u += z2[nt][e];
+            if (!kShared) u += z2[nt][e];
             u = kFp8 ? fmaf(u, qs[nt][e & 1] * ks[e >> 1], lv[e >> 1]) : u * qs[nt][e & 1];
             if (edge && !seen(g + 8 * (e >> 1), tq[nt][e & 1])) u = -INFINITY;
             over |= u > m[nt][e & 1] + kLazy;
@@ -843,32 +884,40 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
 }
 
 // Joins the splits of one (query row, head): M = max m_s, o = sum_s
-// exp2(m_s - M) O_s / (exp2(sink - M) + sum_s exp2(m_s - M) l_s).  One CTA
-// per row.  Warp w takes splits w, w + 8, ..., 32 at a time: a lane reads one
-// split's (m, l) while the outputs are already on their way; the warps'
-// results are then added in order.
+// exp2(m_s - M) O_s / (exp2(sink - M) + sum_s exp2(m_s - M) l_s).  Up to kFew
+// splits are a warp's work, a CTA then takes eight heads (160 x 40 rows of few
+// splits: 15.5 us with a CTA each).  More are a CTA's: warp w takes splits w, w + 8,
+// ..., 32 at a time: a lane reads one split's (m, l) while the outputs are
+// already on their way; the warps' results are then added in order.
+constexpr int kFew = kSplits;  // at most a warp's lanes
 template <bool kBf16, int kD>
 __global__ void __launch_bounds__(256) gqa_join_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int kV = kD / 32;
   __shared__ float red[8][kD];
   __shared__ float red_l[8], red_m[8];
-  const int row = blockIdx.x, h = blockIdx.y, b = row / a.T, tau = row % a.T;
+  const int row = blockIdx.x, b = row / a.T, tau = row % a.T;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // (lens was complete before gqa_decode_kernel let this kernel begin)
   const int n = n_splits(span_of(a, a.lens[b]).n);
-  const float sink = a.sink ? a.sink[h] * kLog2e : -INFINITY;
+  // (the grid has eight heads a CTA where no sequence can have more than kFew)
+  const bool few = n <= kFew;
+  const int heads8 = a.max_splits <= kFew ? 8 * blockIdx.y : blockIdx.y;
+  const int h = few ? heads8 + warp : heads8;
   pdl_wait();
   if (n == 1) return;  // finished by gqa_decode_kernel
+  if (few && ((heads8 & 7) || h >= a.n_heads)) return;
+  const float sink = a.sink ? a.sink[h] * kLog2e : -INFINITY;
   const int64_t stride = (int64_t)a.T * a.n_heads;
   const int64_t slot = (int64_t)b * a.max_splits * stride + tau * a.n_heads + h;
   float acc[kV] = {}, M = -INFINITY, den = 0.f;
-  for (int s0 = warp; s0 < n; s0 += 256) {
-    const int mine = s0 + 8 * lane, count = min(32, (n - s0 + 7) / 8);
+  const int every = few ? 1 : 8;
+  for (int s0 = few ? 0 : warp; s0 < n; s0 += 32 * every) {
+    const int mine = s0 + every * lane, count = min(32, (n - s0 + every - 1) / every);
     const float2 ml = mine < n ? a.part_ml[slot + mine * stride] : make_float2(-INFINITY, 0.f);
     const float* src = a.part_o + (slot + s0 * stride) * kD + kV * lane;
     float buf[4][kV];
     auto load = [&](int i, float (&v)[kV]) {
-      const float* p = src + 8 * i * stride * kD;
+      const float* p = src + every * i * stride * kD;
       if (kV == 4) {
         const float4 x = *reinterpret_cast<const float4*>(p);
         v[0] = x.x; v[1] = x.y; v[kV - 2] = x.z; v[kV - 1] = x.w;
@@ -897,6 +946,16 @@ __global__ void __launch_bounds__(256) gqa_join_kernel(const __grid_constant__ D
           if (i0 + 4 + i < count) load(i0 + 4 + i, buf[i]);
         }
     }
+  }
+  if (few) {
+    if (M != -INFINITY) den += ex2(sink - M);
+    const float inv = den != 0.f ? rcp(den) : 0.f;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)row * a.out.row_stride +
+                    (int64_t)h * a.out.head_stride + kV * lane;
+#pragma unroll
+    for (int j = 0; j < kV; j += 2)
+      *reinterpret_cast<uint32_t*>(dst + j) = pack2<kBf16>(acc[j] * inv, acc[j + 1] * inv);
+    return;
   }
 #pragma unroll
   for (int j = 0; j < kV; ++j) red[warp][kV * lane + j] = acc[j];
@@ -931,8 +990,11 @@ int most_blocks(const gqa_params& p, int T, int n_max) {
   return (int)((keys + kBlock - 1) / kBlock);
 }
 
-// 8 query rows per item where they hold the whole group, else 16.
-int rows_per_item(const gqa_params& p, int T) { return T * (p.n_heads / p.n_kv_heads) <= 8 ? 8 : 16; }
+// 8 or 16 query rows per item where they hold the whole group, else 32.
+int rows_per_item(const gqa_params& p, int T) {
+  const int rows = T * (p.n_heads / p.n_kv_heads);
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
 
 template <bool kBf16, bool kFp8, int kD, int kNq>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeArgs& a, int64_t items, cudaStream_t st) {
@@ -943,7 +1005,8 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeArg
   const int grid = (int)(items < sm_count() ? items : sm_count());
   e = launch_pdl(fn, dim3(grid), dim3(32 * L::kWarps), L::kSmem, st, mk, mv, a);
   if (e != cudaSuccess || a.max_splits == 1) return e;
-  return launch_pdl(gqa_join_kernel<kBf16, kD>, dim3(a.B * a.T, a.n_heads), dim3(256), 0, st, a);
+  const int heads = a.max_splits <= kFew ? (a.n_heads + 7) / 8 : a.n_heads;
+  return launch_pdl(gqa_join_kernel<kBf16, kD>, dim3(a.B * a.T, heads), dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -988,11 +1051,14 @@ cudaError_t launch_gqa_decode(const gqa_params& p, const gqa_rows& q, const gqa_
                      n_max, p.n_heads, p.n_kv_heads, kv_shift, p.page, shift, p.window < (1 << 30) ? p.window : 0, splits, p.softmax_scale * kLog2e, err};
   const int nq = rows_per_item(p, T);
   const int64_t items = gqa_decode_items(p, T, n_max);
-#define GQA_GO(BF, F8)                                                                                              \
-  (p.d == 128 ? (nq == 8 ? launch<BF, F8, 128, 8>(mk, mv, a, items, st) : launch<BF, F8, 128, 16>(mk, mv, a, items, st)) \
-              : (nq == 8 ? launch<BF, F8, 64, 8>(mk, mv, a, items, st) : launch<BF, F8, 64, 16>(mk, mv, a, items, st)))
+#define GQA_ROWS(BF, F8, D)                              \
+  (nq == 8    ? launch<BF, F8, D, 8>(mk, mv, a, items, st)  \
+   : nq == 16 ? launch<BF, F8, D, 16>(mk, mv, a, items, st) \
+              : launch<BF, F8, D, 32>(mk, mv, a, items, st))
+#define GQA_GO(BF, F8) (p.d == 128 ? GQA_ROWS(BF, F8, 128) : GQA_ROWS(BF, F8, 64))
   return bf ? (f8 ? GQA_GO(true, true) : GQA_GO(true, false)) : (f8 ? GQA_GO(false, true) : GQA_GO(false, false));
 #undef GQA_GO
+#undef GQA_ROWS
 }
 
 }  // namespace csa
