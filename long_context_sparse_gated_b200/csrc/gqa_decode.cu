@@ -25,6 +25,13 @@
 //   product  S^T[keys, rows] = K Q^T, P^T = exp2(S^T - m), O^T[d, rows] += V^T P^T
 //            by mma.sync.  With the keys as M, 8 query rows fill an MMA (with
 //            rows as M the usual groups of 8 would waste half of it).
+//   rows     8, 16 or 32 an item, so that several tokens and large groups do not
+//            read the cache twice. With 32 the sums leave no registers for the
+//            queries, whose fragments wait in shared memory.  40 sequences of up
+//            to 1152 keys, 4 tokens, 40 / 8 heads: 48 us, in items of 16 rows 67;
+//            8 of up to 20000, 64 / 8 heads: 117 and 125, FP8 135 and 157.  (Two
+//            warps a scheduler then wait for their own instructions, 4000 clocks a
+//            tile: 117 us are 59% of the copy rate.)
 //
 // 16-bit cache.  m16n8k16; K by ldmatrix, V by ldmatrix.trans, P^T rounded to
 // 16 bits and transposed in registers by movmatrix.
@@ -764,8 +771,10 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
       for (int mt = 0; mt < kD / 16; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][nt][e] *= f[e & 1];
-      // warps 2 and 3 to 0 and 1, then 1 to 0: a lane's registers go to the
-      // same lane
+      // warp nt takes an n-tile over: of the warps in turn from it, the third
+      // and fourth give to it and the second, then the second to it, a lane's
+      // registers to the same lane
+      const int turn = (w4 - nt) & 3;
       if (nt > 0) sm100::named_bar_sync(1 + team, 32 * kTeam);  // the buffer is read
       auto give = [&](int buf) {
 #pragma unroll
@@ -782,13 +791,17 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
           o[mt][nt][3] += v.w;
         }
       };
-      if (w4 >= 2) give(w4 & 1);
+      if (turn >= 2) give(turn & 1);
       sm100::named_bar_sync(1 + team, 32 * kTeam);
-      if (w4 < 2) take(w4);
-      if (w4 == 1) give(1);
+      if (turn < 2) take(turn);
+      if (turn == 1) give(1);
       sm100::named_bar_sync(1 + team, 32 * kTeam);
-      if (w4 != 0) continue;
-      take(1);
+      if (turn == 0) take(1);
+    }
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt) {
+      if (w4 != nt) continue;
+      float f[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         f[e] = 1.f;

@@ -280,6 +280,58 @@ def test_decode_odd_values_reach_only_who_sees_them(lib, act, kv):
     _decode(lib, [50, 200, 67], act, kv, 4, 2, 64, 16, T=3, window=40, v_odd=odd)
 
 
+@pytest.mark.parametrize("act,kv", [("bf16", "act"), ("f16", "act"), ("bf16", "fp8"), ("f16", "fp8")])
+@pytest.mark.parametrize("T,H,G,window", [(1, 17, 1, 0), (3, 11, 1, 500), (4, 40, 8, 0), (8, 32, 8, 33), (33, 2, 2, 0)])
+def test_decode_rows_of_one_item_and_a_few_more(lib, act, kv, T, H, G, window):
+    """17, 20, 32 and 33 query rows a KV head: an item with columns to spare,
+    a full one, one row in a second item."""
+    for d in (64, 128):
+        _decode(lib, [0, 1, 16, 40, 300, 1100], act, kv, H, G, d, 32, T, window, T != 3, seed=T + d)
+
+
+@pytest.mark.parametrize("act,kv", [("bf16", "act"), ("f16", "act"), ("bf16", "fp8")])
+@pytest.mark.parametrize("T,H,G", [(4, 16, 2), (8, 8, 2), (5, 4, 1)])
+def test_decode_odd_values_among_many_rows(lib, act, kv, T, H, G):
+    """As above, with 20 to 32 rows an item."""
+    def odd(vs):
+        vs[0][-1, 0, 5] = float("nan")
+        vs[1][-1, G - 1, 7] = float("nan")
+        vs[1][0] = float("nan")
+        vs[2][-2, 0, 9] = float("nan")
+    for d in (64, 128):
+        _decode(lib, [50, 700, 67], act, kv, H, G, d, 16, T, window=40, v_odd=odd, seed=3)
+    if kv == "act":  # (the helper compares bad pages with rows that were not quantised)
+        _decode(lib, [200, 700], act, kv, H, G, 128, 64, T, bad=[(0, 3), (1, 0), (1, 1), (1, 10)])
+
+
+@pytest.mark.parametrize("act,kv,d", [("bf16", "act", 128), ("f16", "fp8", 64)])
+@pytest.mark.parametrize("T,H,G", [(1, 12, 4), (3, 12, 2)])
+def test_decode_joins_of_few_and_many_splits(lib, act, kv, d, T, H, G):
+    """Twelve splits are joined by a warp, thirteen by a CTA; a batch that
+    holds both, and one whose bound allows only few, give the same bits."""
+    lens = [12288, 300, 12289, 0, 256, 257, 13500]
+    whole = _decode(lib, lens, act, kv, H, G, d, 128, T, seed=11, sink=True)
+    few = [0, 300, 0, 0, 256, 257, 0]
+    ks = [_randn((n, G, d), act, 40 + b) for b, n in enumerate(lens)]
+    vs = [_randn((n, G, d), act, 540 + b) for b, n in enumerate(lens)]
+    c = Paged(ks, vs, 128, kv, act)
+    q = _randn((len(lens) * T, H, d), act, 1).cuda()
+    p = _params(lib, act, kv, B=len(lens), n_heads=H, n_kv_heads=G, d=d, page=128, softmax_scale=d ** -0.5)
+    outs = []
+    for lengths, n_max in ((lens, max(lens)), (few, 300), (few, 12288), (few, max(lens))):
+        ws = torch.full((lib.gqa_decode_attn_workspace_bytes(p, T, n_max),), 255, dtype=torch.uint8, device="cuda")
+        out = torch.full_like(q, 9.0)
+        lib.gqa_decode_attn(p, q, c.handle(), c.table, _i32(lengths), T, n_max, out, ws)
+        outs.append(out.view(len(lens), T, H, d))
+    for b, n in enumerate(few):
+        if n:
+            for x in outs[1:]:
+                assert torch.equal(x[b], outs[0][b]), n
+    for x in outs[1:]:
+        assert not x[[0, 2, 3, 6]].any()
+    assert whole.isfinite().all()
+
+
 @pytest.mark.parametrize("kv", ["act", "fp8"])
 def test_decode_large_and_small_magnitudes(lib, kv):
     """Logits in the hundreds (one key takes all), keys and values of any
