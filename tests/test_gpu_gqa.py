@@ -117,6 +117,13 @@ def test_append(lib, act, kv, H, G, d, r, page):
     _append(lib, act, kv, [1, 0, 37, 2, 130], [0, 5, 13, 131071, 1000], H, G, d, r, page)
 
 
+@pytest.mark.parametrize("act,kv", [("bf16", "act"), ("f16", "fp8"), ("bf16", "fp8"), ("f16", "act")])
+@pytest.mark.parametrize("H,G,d,r", [(32, 8, 128, 64), (28, 7, 128, 128), (16, 4, 64, 64), (9, 1, 64, 32), (128, 64, 128, 128)])
+def test_append_many_tokens(lib, act, kv, H, G, d, r):
+    """Enough tokens for several a CTA, in two and in three pieces a thread."""
+    _append(lib, act, kv, [1100, 1, 0, 398], [7, 0, 3, 50000], H, G, d, r, 64, tail=3, seed=8)
+
+
 @pytest.mark.parametrize("kv", ["act", "fp8"])
 def test_append_one_token_each(lib, kv):
     _append(lib, "bf16", kv, [1] * 33, [17 * i for i in range(33)], 32, 8, 128, 128, 16, seed=3)
