@@ -27,11 +27,11 @@
 //            rows as M the usual groups of 8 would waste half of it).
 //   rows     8, 16 or 32 an item, so that several tokens and large groups do not
 //            read the cache twice. With 32 the sums leave no registers for the
-//            queries, whose fragments wait in shared memory.  40 sequences of up
-//            to 1152 keys, 4 tokens, 40 / 8 heads: 48 us, in items of 16 rows 67;
-//            8 of up to 20000, 64 / 8 heads: 117 and 125, FP8 135 and 157.  (Two
-//            warps a scheduler then wait for their own instructions, 4000 clocks a
-//            tile: 117 us are 59% of the copy rate.)
+//            queries, whose fragments and positions wait in shared memory.  40
+//            sequences of up to 1152 keys, 4 tokens, 40 / 8 heads: 44 us, in items
+//            of 16 rows 67; 8 of up to 20000, 64 / 8 heads: 112 and 125, FP8 122 and
+//            157.  (Two warps a scheduler then wait for their own instructions, some
+//            4000 clocks a tile: 112 us are 62% of the copy rate.)
 //
 // 16-bit cache.  m16n8k16; K by ldmatrix, V by ldmatrix.trans, P^T rounded to
 // 16 bits and transposed in registers by movmatrix.
@@ -227,7 +227,7 @@ struct Layout {
   static constexpr int kSlots = kFp8 ? (kD == 128 ? 32 : 64) : (kD == 128 ? 24 : 48);  // stages of all warps
   static constexpr int kJoin = 2 * kD * 8 * 4;              // a team's buffer: two warps' 8 rows
   static constexpr size_t kSmem = 1024 + (size_t)kSlots * (kStage + kScales) + kTeams * kJoin;
-  static_assert(kSmem + 8192 + 68 * kTeams * kNq <= 232448, "shared memory of a CTA");
+  static_assert(kSmem + 8192 + 72 * kTeams * kNq <= 232448, "shared memory of a CTA");
 };
 
 // An item and the stretch of keys in it that has to be read.
@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
   __shared__ uint16_t order[kMaxB];      // sequences, those with the largest splits first
   __shared__ float red_m[L::kTeams][2][kTeam][kNq], red_l[L::kTeams][2][kTeam][kNq];
   __shared__ float red_q[L::kTeams][kShared ? kNq : 1];  // logit factors of the rows
+  __shared__ int red_t[L::kTeams][kShared ? kNq : 1];    // and their positions
   __shared__ int near_lens[kNear];       // lengths of the first sequences
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
     // chunk * kNq + 8 nt + g = tau * G + head
     uint32_t qf[kShared ? 1 : kNt][kD / 8];
     float qs[kNt][2];  // logit factor of columns 2 q4, 2 q4 + 1
-    int tq[kNt][2];    // their positions (INT_MIN: no row)
+    int tq[kShared ? 1 : kNt][2];  // their positions (INT_MIN: no row)
 #pragma unroll
     for (int x = 0; x < (kShared ? 1 : kNt); ++x) {
       const int nt = kShared ? w4 : x;
@@ -464,7 +465,9 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
         }
       }
     }
+    auto position = [&](int r) { return r < rows ? c.s.len - a.T + r / G : INT32_MIN; };
     if (kShared) {
+      if (q4 == 0) red_t[team][kShared ? 8 * w4 + g : 0] = position(c.chunk * kNq + 8 * w4 + g);
       sm100::named_bar_sync(1 + team, 32 * kTeam);  // the last item's join has read the place
 #pragma unroll
       for (int j = 0; j < kD / 32; ++j)
@@ -477,8 +480,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (kShared) qs[nt][e] = kFp8 ? red_q[team][kShared ? 8 * nt + 2 * q4 + e : 0] : a.scale;
-        const int rc = c.chunk * kNq + 8 * nt + 2 * q4 + e;
-        tq[nt][e] = rc < rows ? c.s.len - a.T + rc / G : INT32_MIN;
+        if (!kShared) tq[kShared ? 0 : nt][e] = position(c.chunk * kNq + 8 * nt + 2 * q4 + e);
       }
     }
 
@@ -513,8 +515,8 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
         // some row does not see it as a whole: keys after the first query, or
         // before the last query's window
         const bool at_edge = key0 + kTile - 1 > c.s.len - a.T || (a.window > 0 && key0 < c.s.len - a.window);
-        auto seen = [&](int k, int tcol) {  // the tile's k-th key
-          const int key = key0 + k;
+        auto seen = [&](int k, int nt, int e) {  // the tile's k-th key by column e of an n-tile
+          const int key = key0 + k, tcol = kShared ? red_t[team][kShared ? 8 * nt + 2 * q4 + e : 0] : tq[kShared ? 0 : nt][e];
           return key <= tcol && (a.window == 0 || key > tcol - a.window);
         };
 
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
             float& u = z[nt][e];
             if (!kShared) u += z2[nt][e];
             u = kFp8 ? fmaf(u, qs[nt][e & 1] * ks[e >> 1], lv[e >> 1]) : u * qs[nt][e & 1];
-            if (edge && !seen(g + 8 * (e >> 1), tq[nt][e & 1])) u = -INFINITY;
+            if (edge && !seen(g + 8 * (e >> 1), nt, e & 1)) u = -INFINITY;
             over |= u > m[nt][e & 1] + kLazy;
           }
         // The running maxima move only when a logit exceeds them by kLazy
@@ -715,7 +717,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
                   for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                      if (seen(k, tq[nt][e])) o[mt][nt][2 * e2 + e] += v;
+                      if (seen(k, nt, e)) o[mt][nt][2 * e2 + e] += v;
                 }
               }
             }
