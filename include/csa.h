@@ -486,7 +486,8 @@ csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
  *   o   = sum_j p_j v_j, written in act_fmt; zeros where no key is seen
  *   q, out      [B*T][n_heads]; out overlaps no input
  *   lens        int32 [B]: keys in the cache, the new tokens included
- *   n_max       host upper bound on lens (n_max <= table_cols * page);
+ *   n_max       host upper bound on lens (n_max <= table_cols * page, and
+ *               below 2^30: CSA_ERR_UNSUPPORTED);
  *               a longer sequence is read up to n_max with CSA_DEV_ERR_RANGE
  *   sink        fp32 [n_heads], or NULL for none
  *   ws          workspace of gqa_decode_attn_workspace_bytes(params, T, n_max);

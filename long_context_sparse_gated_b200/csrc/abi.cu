@@ -355,8 +355,12 @@ csa_status gqa_cache_append(const gqa_params* p, gqa_rows q, gqa_rows k, gqa_row
                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// The decode kernel's positions, spans and windows are 32-bit sums: lengths
+// stay below 2^30, and a window of 2^30 or more is none.
+constexpr int32_t kGqaMaxKeys = (1 << 30) - 1;
+
 size_t gqa_decode_attn_workspace_bytes(const gqa_params* p, int32_t T, int32_t n_max) {
-  if (check_gqa(p) != CSA_OK || T < 1 || T > 64 || n_max < 0) return 0;
+  if (check_gqa(p) != CSA_OK || T < 1 || T > 64 || n_max < 0 || n_max > kGqaMaxKeys) return 0;
   return csa::gqa_decode_workspace_bytes(*p, T, n_max);
 }
 
@@ -366,7 +370,7 @@ csa_status gqa_decode_attn(const gqa_params* p, gqa_rows q, gqa_cache cache, con
   csa_status s = check_gqa(p);
   if (s != CSA_OK) return s;
   if (!lens || T < 1 || n_max < 0) return CSA_ERR_INVALID;
-  if (T > 64) return CSA_ERR_UNSUPPORTED;
+  if (T > 64 || n_max > kGqaMaxKeys) return CSA_ERR_UNSUPPORTED;
   if ((s = check_gqa_cache(p, cache, table, table_cols)) != CSA_OK) return s;
   if (n_max > table_cols * p->page) return CSA_ERR_INVALID;
   if ((s = check_rows(p, q)) != CSA_OK || (s = check_rows(p, out)) != CSA_OK) return s;
