@@ -499,7 +499,11 @@ csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
  * an FP8 value counts as no less than 2^-90 and no more than 2^90.  How a
  * sequence's keys are split depends on its own length, T and the window
  * alone, and partial results are joined in a fixed order: a query's output
- * is bit-identical run to run and whatever batch it is in. */
+ * is bit-identical run to run and whatever batch it is in.  Each exp(z_j) is
+ * rounded before it weighs its value: to BF16 (2^-8 of itself) for a BF16
+ * cache, else to FP16 (2^-11 of itself, or 2^-36 of the query's largest where
+ * that is more; for an FP8 cache this is about exp(z_j) times the value's
+ * scale).  The sums are fp32. */
 csa_status gqa_decode_attn(const gqa_params* params, gqa_rows q, gqa_cache cache,
                            const int32_t* table, int64_t table_cols,
                            const int32_t* lens, int32_t T, int32_t n_max,

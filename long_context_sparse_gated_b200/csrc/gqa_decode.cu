@@ -44,12 +44,16 @@
 // are needed.  A query row is brought into FP16 by a power of two of its own
 // (largest magnitude in [2^14, 2^15); what is 2^29 below that loses bits that do
 // not show in fp32).  The value's scale s_j joins the weight: w_j = exp2(z_j +
-// log2 s_j - M) with M the running maximum of that sum, so weights stay in (0,
-// 2^8] whatever the scales are, and the denominator sums w_j / s_j.  Value
-// scales are read as within 2^-90 .. 2^90.
+// log2 s_j - M) with M following the running maximum of that sum, so weights
+// stay in (0, 2^15] whatever the scales are, and the denominator sums w_j / s_j.
+// Value scales are read as within 2^-90 .. 2^90.
 //
-// Rounding.  Weights are rounded to 16 bits (relative 2^-9 for a BF16 cache,
-// 2^-12 for FP16 and FP8 caches), sums and partial outputs are fp32.
+// Rounding.  Weights are rounded to 16 bits, since that is what the product
+// takes: to BF16 for a BF16 cache (2^-8 of themselves), else to FP16 (2^-11, where
+// FP16 has its full precision: down to 2^-25 of the largest weight, which is 2^11
+// at least; below that by up to 2^-36 of the largest).  The maximum is followed
+// closer for that than for BF16 (by 2^4 instead of 2^8).  Sums and partial outputs
+// are fp32.
 //
 // Masks.  Tiles of pages that are none are passed over.  Tiles that a row
 // does not see as a whole (the last ones, a window's first) take a path of
@@ -72,7 +76,13 @@ constexpr int kTile = 16;   // keys per stage
 constexpr int kBlock = 32;  // keys: splits begin at multiples of it
 constexpr int kMaxStages = 16;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLazy = 8.f;      // base-2 units
+// Weights are 2^(z - m) with m = a running maximum - kTop, raised when a logit
+// exceeds the maximum by kLazy (base-2 units).  FP16 holds weights from 2^-14
+// (with fewer bits from 2^-24) to 2^16, so the largest are put near its top.
+template <bool kBf16>
+struct Weights {
+  static constexpr float kTop = kBf16 ? 0.f : 11.f, kLazy = kBf16 ? 8.f : 4.f;
+};
 constexpr float kNone = -3.0e38f;  // a running maximum before the first key
 struct Edge { static constexpr bool value = true; };
 struct Whole { static constexpr bool value = false; };
@@ -247,6 +257,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
   constexpr bool kShared = kNq == 32;  // the queries' fragments in shared memory
   static_assert(!kShared || kNt == kTeam, "a warp brings one n-tile's");
   constexpr bool kMmaBf16 = kBf16 && !kFp8;
+  constexpr float kTop = Weights<kMmaBf16>::kTop, kOver = kTop + Weights<kMmaBf16>::kLazy;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t full_bar[L::kSlots];
   __shared__ int first_item[kMaxB + 1];  // items before the i-th sequence of the order
@@ -593,10 +604,10 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
             if (!kShared) u += z2[nt][e];
             u = kFp8 ? fmaf(u, qs[nt][e & 1] * ks[e >> 1], lv[e >> 1]) : u * qs[nt][e & 1];
             if (edge && !seen(g + 8 * (e >> 1), nt, e & 1)) u = -INFINITY;
-            over |= u > m[nt][e & 1] + kLazy;
+            over |= u - m[nt][e & 1] > kOver;
           }
-        // The running maxima move only when a logit exceeds them by kLazy
-        // (weights then stay below 2^kLazy): mostly one vote instead of
+        // The references move only when a logit exceeds its maximum by kLazy
+        // (weights then stay below 2^kOver): mostly one vote instead of
         // shuffles over the keys and a pass over O.
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -607,7 +618,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
               float v = fmaxf(z[nt][e], z[nt][e + 2]);
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16)) - kTop;
               alpha[e] = 1.f;
               if (v > m[nt][e]) {
                 alpha[e] = ex2(m[nt][e] - v);  // 0 from kNone

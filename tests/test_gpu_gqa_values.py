@@ -1,0 +1,102 @@
+"""What values can do to the grouped-query attention calls: NaN and infinities
+in keys, queries and values, one key that outweighs thousands, magnitudes at
+the ends of the types, FP8 scales far apart; and calls from two host threads.
+
+Bounds are those of gqa_util; where a value is not finite it has to be the
+same one, sign and all."""
+
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from gqa_util import ACT, Paged, check_out, f64
+from oracle import gqa
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from long_context_sparse_gated_b200 import build
+    build.build()
+    import long_context_sparse_gated_b200 as m
+    return m
+
+
+def _params(lib, act="bf16", kv="act", **kw):
+    return lib.make_gqa_params(act_fmt=lib.ACT_BF16 if act == "bf16" else lib.ACT_F16,
+                               kv_fmt=lib.KV_ACT if kv == "act" else lib.KV_FP8, **kw)
+
+
+def _randn(shape, act, seed, gain=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * gain).to(ACT[act])
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _starts(lens):
+    return _i32([0] + list(np.cumsum(lens)))
+
+
+def _same(got, want, mag, zmag, act, what=""):
+    """check_out, and infinities and NaN exactly as wanted."""
+    got = f64(got)
+    odd = ~np.isfinite(want)
+    np.testing.assert_array_equal(got[odd], want[odd], err_msg=what)
+    check_out(got[~odd], want[~odd], mag[~odd], zmag, act, what)
+
+
+def _prompt(lib, q, k, v, nq, nk, act, scale, window=0, sink=None):
+    """gqa_prompt_attn of CPU rows; the output on the CPU."""
+    H, d = q.shape[1:]
+    p = _params(lib, act, B=len(nq), n_heads=H, n_kv_heads=k.shape[1], d=d, window=window, softmax_scale=scale)
+    out, err = torch.full(q.shape, 9.0, device="cuda").to(q.dtype), torch.zeros(4, dtype=torch.int32, device="cuda")
+    lib.gqa_prompt_attn(p, q.cuda(), k.cuda(), v.cuda(), _starts(nq), _starts(nk), out,
+                        sink=None if sink is None else sink.cuda(), err=err)
+    assert int(err[0]) == 0
+    return out.cpu()
+
+
+def _decode(lib, q, cache, table, lens, T, act, kv, G, page, scale, window=0, sink=None):
+    H, d = q.shape[1:]
+    p = _params(lib, act, kv, B=len(lens), n_heads=H, n_kv_heads=G, d=d, page=page, window=window, softmax_scale=scale)
+    n_max = max(lens)
+    ws = torch.full((max(16, lib.gqa_decode_attn_workspace_bytes(p, T, n_max)),), 255, dtype=torch.uint8, device="cuda")
+    out, err = torch.full(q.shape, 9.0, device="cuda").to(q.dtype), torch.zeros(4, dtype=torch.int32, device="cuda")
+    lib.gqa_decode_attn(p, q.cuda(), cache, table, _i32(lens), T, n_max, out, ws, sink=None if sink is None else sink.cuda(), err=err)
+    assert int(err[0]) == 0
+    return out.cpu()
+
+
+# ---- weights and magnitudes far apart ------------------------------------------
+
+def _sink_like(n, d, act, nats, at, seed):
+    """Keys of which one outweighs the others by e^nats, with a value of zero,
+    among values of one sign."""
+    k, v = _randn((n, 1, d), act, seed, 0.02), (_randn((n, 1, d), act, seed + 1).float().abs() + 0.5).to(ACT[act])
+    k[at] = nats / d ** 0.5
+    v[at] = 0
+    return k, v
+
+
+@pytest.mark.parametrize("act,kv", [("f16", "act"), ("bf16", "act"), ("bf16", "fp8"), ("f16", "fp8")])
+@pytest.mark.parametrize("nats", [8, 12, 14, 16])
+@pytest.mark.parametrize("T,H", [(1, 2), (2, 8), (5, 8)])
+def test_decode_one_key_outweighs_thousands(lib, act, kv, nats, T, H):
+    d, page = 128, 64
+    for m, at in ((300, 2), (2100, 1030), (9000, 0)):
+        k, v = _sink_like(m, d, act, nats, at, 5)
+        if kv == "fp8":
+            v[at, 0, 0] = 1.0  # a scale like the others', codes of zero
+        q = torch.ones(T, H, d).to(ACT[act])
+        c = Paged([k], [v], page, kv, act)
+        out = _decode(lib, q, c.handle(), c.table, [m], T, act, kv, 1, page, d ** -0.5)
+        want, mag, zmag = gqa.attend(f64(q), *c.rows(0, m), np.arange(m - T, m), d ** -0.5)
+        _same(out, want, mag, zmag, act, f"{m} keys")
