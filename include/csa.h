@@ -517,7 +517,8 @@ size_t gqa_decode_attn_workspace_bytes(const gqa_params* params, int32_t T,
  * cu_k[b] .. cu_k[b+1]-1 of k and v; the last query sits at the last key, so
  * query i of n sits at t = (keys - n) + i and sees the keys at
  * max(0, t-window+1) .. t (none where t < 0: its output is zeros).
- * Softmax, sink and output as in gqa_decode_attn.
+ * Softmax, sink and output as in gqa_decode_attn; weights are rounded to
+ * act_fmt (FP16: 2^-11 of themselves, or 2^-34 of the row's largest).
  *   q, out      [n_q][n_heads]; out overlaps no input
  *   k, v        [n_k][n_kv_heads]
  *   cu_q, cu_k  int32 [B+1], not decreasing, first 0, last <= n_q / n_k; output

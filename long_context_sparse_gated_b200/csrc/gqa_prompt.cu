@@ -20,7 +20,8 @@
 //             logits in registers, running maximum, P in 16 bits back to
 //             TMEM, in two halves, so that the product with the first 64 keys
 //             begins while the second half is computed.  The maximum moves
-//             only when a row exceeds it by 2^8, so O is hardly ever rescaled;
+//             only when a row exceeds it by 2^8 (FP16: 2^6), so O is hardly ever
+//             rescaled;
 //             at the end the same threads normalise O and write it out
 //             through shared memory.
 //
@@ -30,7 +31,7 @@
 // 3, 425 with 2, 446 with 1, 474 with none) go through the FMA pipe instead: 2^x =
 // 2^n 2^f with n the nearest integer (by adding 1.5 * 2^23) and a polynomial in f,
 // minimax for the relative error on [-1/2, 1/2]: degree 3, 7.5e-5, before P is
-// rounded to BF16 (2^-9), degree 4, 2.6e-6, before FP16 (2^-12).  n is added to
+// rounded to BF16 (2^-8), degree 4, 2.6e-6, before FP16 (2^-11).  n is added to
 // the exponent field; weights below 2^-126 of the row's largest come out as
 // about that.  Packed fp32 pairs (f32x2) throughout.
 //
@@ -43,7 +44,10 @@
 // cost 2700 clocks a tile.)
 //
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d columns each).
-// Rounding: P to the activation type (relative 2^-9 or 2^-12); the rest fp32.
+// Rounding: P to the activation type, since a product's operands are of one type:
+// to BF16 (2^-8 of itself) or FP16 (2^-11, where FP16 has its full precision: down to
+// 2^-23 of the row's largest weight, which is 2^9.5 at least; below that by up to
+// 2^-34 of the largest).  The rest is fp32.
 #include <cuda.h>
 
 #include <cmath>
@@ -61,7 +65,15 @@ using namespace gqa;
 constexpr int kTile = 128;  // query positions of a unit, keys of a tile
 constexpr int kThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLazy = 8.f;  // base-2 units
+// Weights are 2^(z - m + kTop) with m a running maximum, raised when a logit
+// exceeds it by kLazy (base-2 units).  FP16 holds weights from 2^-14 (with fewer bits
+// from 2^-24) to 2^16, so the largest are put near its top, the nearer the closer the
+// maximum is followed (16K tokens, FP16, 8/1 heads of 128: by 2^8 430 us, 2^6 432, 2^4
+// 451).
+template <bool kBf16>
+struct Weights {
+  static constexpr float kTop = kBf16 ? 0.f : 9.5f, kLazy = kBf16 ? 8.f : 6.f;
+};
 
 struct PromptArgs {
   gqa_rows q, k, v, out;
@@ -485,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = warp >> 2, r = (warp & 3) * 32 + lane;
     const Unit u = i ? un[1] : un[0];
     constexpr int kPoly = kBf16 ? 3 : 2;
+    constexpr float kTop = Weights<kBf16>::kTop;
     const int work = i ? work1 : work0;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + 128 * i + lanes, o_col = tmem + 256 + kD * i + lanes;
@@ -541,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const bool over = top > m + a.step;
+      const bool over = top - m > a.step;
       if (__any_sync(0xffffffffu, over)) {
         const float alpha = over ? ex2((m - top) * a.scale) : 1.f;  // 0 from -inf
         if (over) m = top;
@@ -560,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const float mc = m == -INFINITY ? 0.f : m * a.scale;
+      const float mc = m == -INFINITY ? 0.f : m * a.scale - kTop;
       const uint64_t scale2 = f32x2(a.scale, a.scale), mc2 = f32x2(-mc, -mc);
       uint64_t sum2[2] = {0, 0};
       auto weights = [&](auto poly) {
@@ -608,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::tc_fence_after();
     }
     if (u.rows > 0) {
-      if (a.sink && m != -INFINITY) l += ex2(a.sink[u.head] * kLog2e - m * a.scale);
+      if (a.sink && m != -INFINITY) l += ex2(a.sink[u.head] * kLog2e - (m * a.scale - kTop));
       const float f = l != 0.f ? rcp(l) : 0.f;
       uint32_t top = 0;  // largest magnitude of the row, as bits
       constexpr int kChunks = kD / 8;  // 16-byte pieces of a row
@@ -699,7 +712,8 @@ cudaError_t launch_gqa_prompt(const gqa_params& p, const gqa_rows& q, const gqa_
     return cudaErrorInvalidValue;
   const float scale = p.softmax_scale * kLog2e;
   const PromptArgs a{q, k, v, out, (int)n_q, (int)n_k, cu_q, cu_k, sink, p.B, p.n_heads, p.n_kv_heads,
-                     p.window < (1 << 30) ? p.window : 0, scale, fminf(kLazy / scale, 3.0e38f), err};
+                     p.window < (1 << 30) ? p.window : 0, scale,
+                     fminf((bf ? Weights<true>::kLazy : Weights<false>::kLazy) / scale, 3.0e38f), err};
   // the most pairs of units that B sequences of n_q queries can have
   const int64_t G = p.n_heads / p.n_kv_heads, tiles = n_q / kTile + (n_q < p.B ? n_q : p.B);
   const int64_t blocks = (tiles * G + p.B + 1) / 2 * p.n_kv_heads;

@@ -86,6 +86,21 @@ def _sink_like(n, d, act, nats, at, seed):
     return k, v
 
 
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("nats", [8, 12, 14, 16])
+@pytest.mark.parametrize("at", [0, 1030])
+def test_prompt_one_key_outweighs_thousands(lib, act, nats, at):
+    """What the others hold comes out with the accuracy of its own sum: their
+    weights, 2^-23 of the largest, keep the activation type's precision."""
+    for n, m, d in ((2100, 2100, 64), (5, 16384, 128)):
+        q = torch.ones(n, 2, d).to(ACT[act])
+        k, v = _sink_like(m, d, act, nats, at, 5)
+        out = _prompt(lib, q, k, v, [n], [m], act, d ** -0.5)
+        t = np.arange(m - n, m)
+        want, mag, zmag = gqa.attend(f64(q), f64(k), f64(v), t, d ** -0.5)
+        _same(out, want, mag, zmag, act, f"{n} queries, {m} keys")
+
+
 @pytest.mark.parametrize("act,kv", [("f16", "act"), ("bf16", "act"), ("bf16", "fp8"), ("f16", "fp8")])
 @pytest.mark.parametrize("nats", [8, 12, 14, 16])
 @pytest.mark.parametrize("T,H", [(1, 2), (2, 8), (5, 8)])
