@@ -32,8 +32,8 @@
 // 2^n 2^f with n the nearest integer (by adding 1.5 * 2^23) and a polynomial in f,
 // minimax for the relative error on [-1/2, 1/2]: degree 3, 7.5e-5, before P is
 // rounded to BF16 (2^-8), degree 4, 2.6e-6, before FP16 (2^-11).  n is added to
-// the exponent field; weights below 2^-126 of the row's largest come out as
-// about that.  Packed fp32 pairs (f32x2) throughout.
+// the exponent field; weights below 2^-126 (2^-98 of the row's largest and less)
+// come out as about that.  Packed fp32 pairs (f32x2) throughout.
 //
 // Masks.  In tiles that some row does not see as a whole logits are selected,
 // blocks of 32 keys that a warp's rows all see or all miss at once.  A value
@@ -69,10 +69,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 // exceeds it by kLazy (base-2 units).  FP16 holds weights from 2^-14 (with fewer bits
 // from 2^-24) to 2^16, so the largest are put near its top, the nearer the closer the
 // maximum is followed (16K tokens, FP16, 8/1 heads of 128: by 2^8 430 us, 2^6 432, 2^4
-// 451).
+// 451).  BF16 weights stay below 2^-20, so that sums of the type's largest values over
+// 2^20 keys are finite.
 template <bool kBf16>
 struct Weights {
-  static constexpr float kTop = kBf16 ? 0.f : 9.5f, kLazy = kBf16 ? 8.f : 6.f;
+  static constexpr float kTop = kBf16 ? -28.f : 9.5f, kLazy = kBf16 ? 8.f : 6.f;
 };
 
 struct PromptArgs {

@@ -115,3 +115,20 @@ def test_decode_one_key_outweighs_thousands(lib, act, kv, nats, T, H):
         out = _decode(lib, q, c.handle(), c.table, [m], T, act, kv, 1, page, d ** -0.5)
         want, mag, zmag = gqa.attend(f64(q), *c.rows(0, m), np.arange(m - T, m), d ** -0.5)
         _same(out, want, mag, zmag, act, f"{m} keys")
+
+
+@pytest.mark.parametrize("act,d", [("bf16", 64), ("bf16", 128), ("f16", 64), ("f16", 128)])
+def test_values_at_the_end_of_the_type(lib, act, d):
+    """Averages of the type's largest values are such values, not infinities."""
+    n, H, G, page = 700, 4, 2, 32
+    top = torch.finfo(ACT[act]).max
+    q, k = _randn((n, H, d), act, 1), _randn((n, G, d), act, 2)
+    v = (_randn((n, G, d), act, 3).float().abs().clamp(0.25, 1.0) * (0.98 * top)).to(ACT[act])
+    v[:, 0] = 0.75 * top
+    out = _prompt(lib, q, k, v, [n], [n], act, d ** -0.5)
+    want, mag, zmag = gqa.attend(f64(q), f64(k), f64(v), np.arange(n), d ** -0.5)
+    _same(out, want, mag, zmag, act, "prompt")
+    c = Paged([k], [v], page, "act", act)
+    for T in (1, 9):
+        out = _decode(lib, q[-T:], c.handle(), c.table, [n], T, act, "act", G, page, d ** -0.5)
+        _same(out, want[-T:], mag[-T:], zmag, act, "decode")
