@@ -495,7 +495,8 @@ csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
  *               need one each
  * T is at most 64.  The keys of a page not in [0, n_pages) are skipped with
  * CSA_DEV_ERR_INDEX.  What masked slots hold (infinities and NaN included)
- * does not matter; logits of seen keys must be finite in fp32.  The scale of
+ * does not matter; logits of seen keys must be finite in fp32 (one that is
+ * NaN or +infinity makes its query's output NaN).  The scale of
  * an FP8 value counts as no less than 2^-90 and no more than 2^90.  How a
  * sequence's keys are split depends on its own length, T and the window
  * alone, and partial results are joined in a fixed order: a query's output

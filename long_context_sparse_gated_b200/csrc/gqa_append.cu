@@ -51,13 +51,6 @@ struct AppendArgs {
   double turns[64];  // theta^(-2j/r) / 2 pi
 };
 
-// The larger, or NaN if one of them is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // The sequence that packed row i belongs to: the last b with cu[b] <= i (so
 // that empty sequences are passed over), or -1 when i >= cu[B].  A warp
 // narrows 32 ways at a time.

@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 4; c < 128; c += 4)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int e = 0; e < 4; ++e) mx[e] = max_nan(mx[e], s[c + e]);
+      const float top = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
       const bool over = top - m > a.step;
       if (__any_sync(0xffffffffu, over)) {
         const float alpha = over ? ex2((m - top) * a.scale) : 1.f;  // 0 from -inf
@@ -614,6 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       split2(sum2[0], a0, a1);
       split2(sum2[1], a2, a3);
       l += (a0 + a1) + (a2 + a3);
+      // a logit that is NaN or +infinity makes the row NaN (the polynomial alone
+      // would take it for a small weight)
+      if (!(top < INFINITY)) l = NAN;
     }
 
     // ---- output

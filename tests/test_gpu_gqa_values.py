@@ -75,6 +75,99 @@ def _decode(lib, q, cache, table, lens, T, act, kv, G, page, scale, window=0, si
     return out.cpu()
 
 
+# ---- NaN in keys and queries ---------------------------------------------------
+
+@pytest.mark.parametrize("act,d", [("bf16", 128), ("f16", 128), ("bf16", 64), ("f16", 64)])
+def test_prompt_nan_in_a_key_at_every_column(lib, act, d):
+    """The last four queries of 300 keys see two tiles of 128 whole and a part
+    of a third; a NaN in any one key makes every row that sees it NaN, and the
+    heads of the other KV head stay exact."""
+    cols = list(range(256)) + [256, 270, 298]
+    n, m, H, G = 4, 300, 2, 2
+    B = len(cols)
+    q, k, v = _randn((n * B, H, d), act, 1), _randn((m * B, G, d), act, 2), _randn((m * B, G, d), act, 3)
+    bad = k.clone()
+    for b, c in enumerate(cols):
+        bad[b * m + c, 0, (7 * c) % d] = float("nan")
+    out = _prompt(lib, q, bad, v, [n] * B, [m] * B, act, d ** -0.5)
+    for b, c in enumerate(cols):
+        t = np.arange(m - n, m)
+        want, mag, zmag = gqa.attend(f64(q[b * n:(b + 1) * n]), f64(k[b * m:(b + 1) * m]), f64(v[b * m:(b + 1) * m]), t, d ** -0.5)
+        want[t >= c, 0] = np.nan
+        _same(out[b * n:(b + 1) * n], want, mag, zmag, act, f"key {c}")
+
+
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_prompt_infinite_logit_is_not_hidden(lib, act):
+    """A logit of +infinity makes its rows NaN, wherever the key lies."""
+    n, m, d = 2, 300, 64
+    cols = list(range(0, 298, 3))
+    B = len(cols)
+    q, k, v = _randn((n * B, 1, d), act, 1), _randn((m * B, 1, d), act, 2), _randn((m * B, 1, d), act, 3)
+    q[:, 0, 5] = 1.0
+    for b, c in enumerate(cols):
+        k[b * m + c, 0, 5] = float("inf")
+    assert _prompt(lib, q, k, v, [n] * B, [m] * B, act, d ** -0.5).isnan().all()
+
+
+@pytest.mark.parametrize("act,d", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("window", [0, 70])
+def test_prompt_nan_in_keys_and_queries_reach_only_who_sees_them(lib, act, d, window):
+    nq, H, G = [300, 290], 4, 2
+    q, k, v = _randn((590, H, d), act, 1), _randn((590, G, d), act, 2), _randn((590, G, d), act, 3)
+    bad_q, bad_k = q.clone(), k.clone()
+    bad_q[150, 3, 0] = bad_q[0, 0, 1] = float("nan")
+    bad_k[40, 0, 3] = bad_k[299, 1, 5] = bad_k[300 + 130, 1, 0] = float("nan")
+    out = _prompt(lib, bad_q, bad_k, v, nq, nq, act, d ** -0.5, window)
+    at = 0
+    for n in nq:
+        t = np.arange(n)
+        want, mag, zmag = gqa.attend(f64(q[at:at + n]), f64(k[at:at + n]), f64(v[at:at + n]), t, d ** -0.5, window)
+        want[np.isnan(f64(bad_q[at:at + n])).any(-1)] = np.nan
+        for j, g in np.argwhere(np.isnan(f64(bad_k[at:at + n])).any(-1)):
+            rows = (t >= j) & ((t < j + window) if window else True)
+            want[rows, g * (H // G):(g + 1) * (H // G)] = np.nan
+        _same(out[at:at + n], want, mag, zmag, act, f"sequence at {at}")
+        at += n
+
+
+@pytest.mark.parametrize("act,kv", [("bf16", "act"), ("f16", "act"), ("bf16", "fp8")])
+@pytest.mark.parametrize("T,H", [(1, 4), (3, 8), (5, 8)])
+def test_decode_nan_in_keys_and_queries_reach_only_who_sees_them(lib, act, kv, T, H):
+    G, d, page, window = 2, 128, 16, 40
+    lens = [50, 700, 67]
+    ks, vs = ([_randn((n, G, d), act, s + b) for b, n in enumerate(lens)] for s in (1, 50))
+    q = _randn((len(lens) * T, H, d), act, 3)
+    clean = Paged(ks, vs, page, kv, act)
+    bad = [x.clone() for x in ks]
+    bad[0][-1, 0, 5] = bad[1][-1, 1, 7] = bad[1][3, 0, 0] = bad[2][30, 1, 9] = float("nan")
+    c, bad_q = Paged(bad, vs, page, kv, act), q.clone()
+    bad_q[T - 1, H - 1, 4] = float("nan")
+    for w in (0, window):
+        out = _decode(lib, bad_q, c.handle(), c.table, lens, T, act, kv, G, page, d ** -0.5, w)
+        for b, n in enumerate(lens):
+            t = np.arange(n - T, n)
+            want, mag, zmag = gqa.attend(f64(q[b * T:(b + 1) * T]), *clean.rows(b, n), t, d ** -0.5, w)
+            want[np.isnan(f64(bad_q[b * T:(b + 1) * T])).any(-1)] = np.nan
+            for j, g in np.argwhere(np.isnan(f64(bad[b])).any(-1)):
+                rows = (t >= j) & ((t < j + w) if w else True)
+                want[rows, g * (H // G):(g + 1) * (H // G)] = np.nan
+            _same(out[b * T:(b + 1) * T], want, mag, zmag, act, f"length {n}, window {w}")
+
+
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [40, 3000])
+def test_decode_infinite_logit_is_not_hidden(lib, act, n):
+    d, page = 128, 32
+    q = _randn((2, 4, d), act, 1)
+    q[:, :, 5] = 1.0
+    for at in (0, 17, n - 2):
+        k, v = _randn((n, 1, d), act, 2), _randn((n, 1, d), act, 3)
+        k[at, 0, 5] = float("inf")
+        c = Paged([k], [v], page, "act", act)
+        assert _decode(lib, q, c.handle(), c.table, [n], 2, act, "act", 1, page, d ** -0.5).isnan().all()
+
+
 # ---- weights and magnitudes far apart ------------------------------------------
 
 def _sink_like(n, d, act, nats, at, seed):
