@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_col = tmem + 128 * i + lanes, o_col = tmem + 256 + kD * i + lanes;
     const int t = u.t0 + r;
     float m = -INFINITY, l = 0.f;  // m in units of S
+    bool far = false;              // some row's maximum is 2^20 or more away from 0
     for (int n = 0; n < work; ++n) {
       const int key0 = (u.j0 + n) * kTile;
       float s[128];
@@ -559,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (__any_sync(0xffffffffu, over)) {
         const float alpha = over ? ex2((m - top) * a.scale) : 1.f;  // 0 from -inf
         if (over) m = top;
+        far = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * a.scale) > 1048576.f);
         l *= alpha;
         if (n > 0) {
           // S being here says that the products before it are done
@@ -574,7 +576,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const float mc = m == -INFINITY ? 0.f : m * a.scale - kTop;
+      float mc = m == -INFINITY ? 0.f : m * a.scale - kTop;
+      if (far) {
+        // the rounding of m * scale would move all weights of the row by a factor,
+        // up to out of the type's range: differences first
+        const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] -= mr;
+        mc = m == -INFINITY ? 0.f : -kTop;
+      }
       const uint64_t scale2 = f32x2(a.scale, a.scale), mc2 = f32x2(-mc, -mc);
       uint64_t sum2[2] = {0, 0};
       auto weights = [&](auto poly) {

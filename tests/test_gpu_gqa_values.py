@@ -225,3 +225,17 @@ def test_values_at_the_end_of_the_type(lib, act, d):
     for T in (1, 9):
         out = _decode(lib, q[-T:], c.handle(), c.table, [n], T, act, "act", G, page, d ** -0.5)
         _same(out, want[-T:], mag[-T:], zmag, act, "decode")
+
+
+@pytest.mark.parametrize("act,size", [("f16", 6e4), ("bf16", 3e3), ("bf16", 1e9), ("bf16", 5e17)])
+def test_equal_logits_of_any_size(lib, act, size):
+    """Logits of up to 10^37, all equal: the average of the values."""
+    n, H, d = 300, 2, 128
+    q, k = torch.full((n, H, d), size).to(ACT[act]), torch.full((n, H, d), size).to(ACT[act])
+    q[:, 1] *= -1
+    v = _randn((n, H, d), act, 3)
+    want = np.cumsum(f64(v), 0) / np.arange(1, n + 1)[:, None, None]
+    mag = np.cumsum(np.abs(f64(v)), 0) / np.arange(1, n + 1)[:, None, None]
+    _same(_prompt(lib, q, k, v, [n], [n], act, 1.0), want, mag, 0.0, act, "prompt")
+    c = Paged([k], [v], 16, "act", act)
+    _same(_decode(lib, q[-3:], c.handle(), c.table, [n], 3, act, "act", H, 16, 1.0), want[-3:], mag[-3:], 0.0, act, "decode")
