@@ -39,9 +39,8 @@
 // blocks of 32 keys that a warp's rows all see or all miss at once.  A value
 // that is not finite where a row's weight is 0 would still reach the row's sum
 // (0 * NaN is NaN): rows behind the sequence are cleared in shared memory, and
-// a row that comes out as something not finite is computed again on its own,
-// from the keys it sees.  (Looking through the value tiles before the products
-// cost 2700 clocks a tile.)
+// rows that come out as something not finite are looked at again (rows_again).
+// (Looking through the value tiles before the products cost 2700 clocks a tile.)
 //
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d columns each).
 // Rounding: P to the activation type, since a product's operands are of one type:
@@ -221,10 +220,171 @@ struct Unit {
   int j0, j1;      // key tiles [j0, j1)
 };
 
-// One row (packed query row `row`, at position t) on its own, by a warp: the
-// path for rows that came out as something not finite.
+// Whether one of eight values is an infinity or NaN.
+template <bool kBf16>
+__device__ __forceinline__ bool odd8(const uint4& v) {
+  constexpr uint32_t e = kBf16 ? 0x7F80u : 0x7C00u, low = kBf16 ? 0x80u : 0x400u;
+  // (an exponent of all ones carries into the sign's place)
+  auto top = [](uint32_t x) { return (x & (e | e << 16)) + (low | low << 16); };
+  return ((top(v.x) | top(v.y) | top(v.z) | top(v.w)) & 0x80008000u) != 0;
+}
+
+// Rows of a unit that came out as something not finite (32 rows from packed query row
+// `row` and position `t` on, `odd` says which), looked at again by their warp.  They
+// stay as they are unless a value that is not finite lies in one of the unit's tiles
+// (keys [key0, key1)) where not all of them see it; it has then reached rows that do
+// not see it as 0 * NaN.  Such rows are computed again, 16 rows by 16 keys at a time
+// with mma.sync and operands straight from global memory; values that are not finite
+// are taken out of blocks that a row does not see as a whole and given to the rows that
+// see them.  6000 tokens of 8/1 heads of 128, us: 110 without such values, 111 with a
+// NaN in the first, 2010 in the last (one unit a head, 32 rows each of its warps), 2170
+// in every one; row by row and key by key the last three take 83000.
 template <bool kBf16, int kD>
-__device__ __noinline__ void one_row(const PromptArgs& a, int row, int t, int head, int kvh, int k0, int lane) {
+__device__ __noinline__ void blocks_again(const PromptArgs& a, unsigned rows, int row0, int t0, int head, int kvh, int k_begin,
+                                        int key0, int key1, int lane) {
+  constexpr float kTop = Weights<kBf16>::kTop;
+  const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q.ptr) + row0 * a.q.row_stride + head * a.q.head_stride;
+  const uint16_t* kp = reinterpret_cast<const uint16_t*>(a.k.ptr) + k_begin * a.k.row_stride + kvh * a.k.head_stride;
+  const uint16_t* vp = reinterpret_cast<const uint16_t*>(a.v.ptr) + k_begin * a.v.row_stride + kvh * a.v.head_stride;
+  const int r0 = __ffs(rows) - 1, r1 = 31 - __clz(rows), window = a.window;
+  // ---- keys that the first of them does not see, or the last one does not any more
+  bool some = false;
+  auto look = [&](int from, int to) {
+    for (int key = from + lane; key < to; key += 32)
+      for (int i = 0; i < kD / 8; ++i) some |= odd8<kBf16>(reinterpret_cast<const uint4*>(vp + key * a.v.row_stride)[i]);
+  };
+  look(max(key0, t0 + r0 + 1), key1);
+  if (window > 0) look(key0, min(key1, t0 + r1 - window + 1));
+  if (!__any_sync(0xffffffffu, some)) return;
+
+  const int g = lane >> 2, q4 = lane & 3;
+#pragma unroll 1
+  for (int half = 0; half < 32; half += 16) {
+    const unsigned here = rows >> half & 0xFFFFu;
+    if (!here) continue;
+    // fragments' rows g and g + 8; rows that are not asked for count as the nearest
+    // that are, so that none is read that is not there
+    const int h0 = half + __ffs(here) - 1, h1 = half + 31 - __clz(here);
+    int t[2];
+    uint32_t qf[kD / 16][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = min(max(half + g + 8 * e, h0), h1);
+      t[e] = t0 + row;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(qp + row * a.q.row_stride) + q4;
+#pragma unroll
+      for (int c = 0; c < kD / 16; ++c) {
+        qf[c][e] = src[8 * c];
+        qf[c][2 + e] = src[8 * c + 4];
+      }
+    }
+    const int first = window > 0 ? max(0, t0 + h0 - window + 1) : 0;  // of their keys
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[kD / 8][4];
+#pragma unroll
+    for (int c = 0; c < kD / 8; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
+#pragma unroll 1
+    for (int key = first & ~15; key <= t0 + h1; key += 16) {
+      auto seen = [&](int j, int e) { return j <= t[e] && (window == 0 || j > t[e] - window); };
+      auto at = [&](int j) { return (int64_t)min(max(j, first), t0 + h1); };  // a key that is there
+      float s[2][4] = {};
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(kp + at(key + 8 * n + g) * a.k.row_stride) + q4;
+#pragma unroll
+        for (int c = 0; c < kD / 16; ++c) mma16816<kBf16>(s[n], qf[c], src[8 * c], src[8 * c + 4]);
+      }
+      bool edge = false;
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool see = seen(key + 8 * n + 2 * q4 + (e & 1), e >> 1);
+          edge |= !see;
+          if (!see) s[n][e] = -INFINITY;
+          top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+        }
+      edge = __any_sync(0xffffffffu, edge);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+        const float alpha = top[e] > m[e] ? ex2((m[e] - top[e]) * a.scale) : 1.f;
+        m[e] = fmaxf(m[e], top[e]);
+        l[e] *= alpha;
+#pragma unroll
+        for (int c = 0; c < kD / 8; ++c) {
+          o[c][2 * e] *= alpha;
+          o[c][2 * e + 1] *= alpha;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mr = m[e >> 1] == -INFINITY ? 0.f : m[e >> 1];
+          s[n][e] = ex2(fmaf(s[n][e] - mr, a.scale, kTop));
+          l[e >> 1] += s[n][e];
+        }
+      const uint32_t pf[4] = {pack2<kBf16>(s[0][0], s[0][1]), pack2<kBf16>(s[0][2], s[0][3]),
+                              pack2<kBf16>(s[1][0], s[1][1]), pack2<kBf16>(s[1][2], s[1][3])};
+      const uint16_t* src[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) src[e] = vp + at(key + 2 * q4 + (e & 1) + 8 * (e >> 1)) * a.v.row_stride + g;
+      bool odd = false;
+#pragma unroll
+      for (int c = 0; c < kD / 8; ++c) {
+        uint32_t b[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          b[e] = (uint32_t)src[2 * e][8 * c] | (uint32_t)src[2 * e + 1][8 * c] << 16;
+          if (edge) {
+            const uint32_t bad = odd_halves<kBf16>(b[e]);
+            odd |= bad != 0;
+            b[e] &= ~bad;
+          }
+        }
+        mma16816<kBf16>(o[c], pf, b[0], b[1]);
+      }
+      if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+        for (int j = key; j < key + 16; ++j) {
+          const uint32_t* v = reinterpret_cast<const uint32_t*>(vp + at(j) * a.v.row_stride) + q4;
+#pragma unroll
+          for (int c = 0; c < kD / 8; ++c) {
+            const float2 x = unpack2<kBf16>(v[4 * c]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (seen(j, e) && !(fabsf(x.x) < INFINITY)) o[c][2 * e] += x.x;
+              if (seen(j, e) && !(fabsf(x.y) < INFINITY)) o[c][2 * e + 1] += x.y;
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (a.sink && m[e] != -INFINITY) l[e] += ex2(a.sink[head] * kLog2e - (m[e] * a.scale - kTop));
+      const float f = l[e] != 0.f ? rcp(l[e]) : 0.f;
+      if (here >> (g + 8 * e) & 1) {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out.ptr) + (int64_t)(row0 + half + g + 8 * e) * a.out.row_stride +
+                                                    head * a.out.head_stride) + q4;
+#pragma unroll
+        for (int c = 0; c < kD / 8; ++c) dst[4 * c] = pack2<kBf16>(o[c][2 * e] * f, o[c][2 * e + 1] * f);
+      }
+    }
+  }
+}
+
+// A lone such row near a sequence's beginning is computed by itself, a lane with kD/32
+// dims of it.  (16 keys take it as long as blocks_again, and with this path in it the
+// kernel around takes 416 us for 16K tokens instead of 440.)
+template <bool kBf16, int kD>
+__device__ __noinline__ void rows_again(const PromptArgs& a, unsigned odd, int key0, int key1, int row, int t, int head, int kvh,
+                                        int k0, int lane) {
+  constexpr float kTop = Weights<kBf16>::kTop;
   constexpr int n = kD / 32;
   auto load = [&](const gqa_rows& s, int64_t row, int h, float (&x)[n]) {
 #pragma unroll
@@ -235,6 +395,12 @@ __device__ __noinline__ void one_row(const PromptArgs& a, int row, int t, int he
       x[j + 1] = f.y;
     }
   };
+  if ((odd & (odd - 1)) || t >= 16) {
+    blocks_again<kBf16, kD>(a, odd, row, t, head, kvh, k0, key0, key1, lane);
+    return;
+  }
+  row += __ffs(odd) - 1;
+  t += __ffs(odd) - 1;
   const int first = a.window > 0 ? max(0, t - a.window + 1) : 0;
   float q[n], x[n], o[n] = {}, m = -INFINITY, l = 0.f;
   load(a.q, row, head, q);
@@ -244,14 +410,14 @@ __device__ __noinline__ void one_row(const PromptArgs& a, int row, int t, int he
 #pragma unroll
     for (int e = 0; e < n; ++e) z = fmaf(q[e], x[e], z);
     z = warp_sum(z) * a.scale;
-    const float mn = fmaxf(m, z), f = m == -INFINITY ? 0.f : ex2(m - mn), p = ex2(z - mn);
+    const float mn = fmaxf(m, z), f = m == -INFINITY ? 0.f : ex2(m - mn), p = ex2(z - mn + kTop);
     load(a.v, k0 + j, kvh, x);
     l = l * f + p;
 #pragma unroll
-    for (int e = 0; e < n; ++e) o[e] = fmaf(p, x[e], f == 0.f ? 0.f : o[e] * f);
+    for (int e = 0; e < n; ++e) o[e] = fmaf(p, x[e], o[e] * f);
     m = mn;
   }
-  if (a.sink && m != -INFINITY) l += ex2(a.sink[head] * kLog2e - m);
+  if (a.sink && m != -INFINITY) l += ex2(a.sink[head] * kLog2e - m + kTop);
   const float inv = l != 0.f ? rcp(l) : 0.f;
 #pragma unroll
   for (int e = 0; e < n; e += 2)
@@ -676,11 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        for (unsigned odd = __ballot_sync(0xffffffffu, r < u.rows && top >= 0x7F800000u); odd; odd &= odd - 1)
-          {
-          const int x = (warp & 3) * 32 + __ffs(odd) - 1;
-          one_row<kBf16, kD>(a, u.row0 + x, u.t0 + x, u.head, kvh, k_begin, lane);
-        }
+        const unsigned odd = __ballot_sync(0xffffffffu, r < u.rows && top >= 0x7F800000u);
+        if (odd) rows_again<kBf16, kD>(a, odd, u.j0 * kTile, min(u.j1 * kTile, n_k), u.row0 + (warp & 3) * 32, t - lane, u.head, kvh, k_begin, lane);
       }
     }
   }

@@ -168,6 +168,100 @@ def test_decode_infinite_logit_is_not_hidden(lib, act, n):
         assert _decode(lib, q, c.handle(), c.table, [n], 2, act, "act", 1, page, d ** -0.5).isnan().all()
 
 
+# ---- values that are not finite ------------------------------------------------
+
+@pytest.mark.parametrize("act,d", [("bf16", 128), ("f16", 64), ("f16", 128)])
+@pytest.mark.parametrize("window", [0, 100, 300])
+def test_prompt_infinities_in_values(lib, act, d, window):
+    """Infinities arrive with their signs (two of opposite signs as NaN), on
+    both sides of tile borders, and only at rows that see them."""
+    nq, H, G = [700, 290, 64], 4, 2
+    q, k, v = _randn((1054, H, d), act, 1), _randn((1054, G, d), act, 2), _randn((1054, G, d), act, 3)
+    inf = float("inf")
+    for row, g, dim, x in ((0, 0, 1, inf), (127, 1, 2, -inf), (128, 1, 2, inf), (255, 0, 63, -inf), (256, 0, 0, float("nan")),
+                           (511, 1, 9, inf), (640, 0, 33, -inf), (699, 1, 4, inf), (700, 0, 5, -inf), (989, 1, 6, inf), (990, 1, 7, inf)):
+        v[row, g, dim] = x
+    out = _prompt(lib, q, k, v, nq, nq, act, d ** -0.5, window)
+    at = 0
+    for n in nq:
+        want, mag, zmag = gqa.attend(f64(q[at:at + n]), f64(k[at:at + n]), f64(v[at:at + n]), np.arange(n), d ** -0.5, window)
+        _same(out[at:at + n], want, mag, zmag, act, f"sequence at {at}")
+        at += n
+
+
+def test_prompt_infinities_in_values_more_keys_and_an_odd_group(lib):
+    """Positions that do not begin at a tile, units of neighbouring position
+    tiles in one CTA (a group of one and of three heads)."""
+    inf = float("inf")
+    for H, G, act, d in ((2, 2, "bf16", 128), (3, 1, "f16", 64)):
+        for window in (0, 200):
+            nq, nk = [400, 9], [577, 333]
+            q, k, v = _randn((409, H, d), act, 1), _randn((910, G, d), act, 2), _randn((910, G, d), act, 3)
+            for row, dim, x in ((3, 1, inf), (176, 2, -inf), (177, 3, inf), (305, 4, -inf), (383, 5, inf), (384, 6, float("nan")),
+                                (576, 7, -inf), (577, 8, inf), (900, 9, inf), (909, 10, -inf)):
+                v[row, :, dim] = x
+            out = _prompt(lib, q, k, v, nq, nk, act, d ** -0.5, window)
+            aq = ak = 0
+            for n, m in zip(nq, nk):
+                want, mag, zmag = gqa.attend(f64(q[aq:aq + n]), f64(k[ak:ak + m]), f64(v[ak:ak + m]), np.arange(m - n, m), d ** -0.5, window)
+                _same(out[aq:aq + n], want, mag, zmag, act, f"{n} of {m}, window {window}")
+                aq, ak = aq + n, ak + m
+
+
+@pytest.mark.parametrize("act,d", [("bf16", 128), ("f16", 64)])
+def test_prompt_one_query_behind_a_value_that_is_not_finite(lib, act, d):
+    """A single query with a window, odd values before it, inside it and in
+    both places, after a few keys and after many."""
+    H, G, inf = 4, 2, float("inf")
+    nk = [2, 5, 12, 16, 17, 40, 130, 300]
+    B = len(nk)
+    at = np.cumsum([0] + nk)
+    sink = torch.tensor([0.5, -1.0, 2.0, 0.0])
+    for window, back in ((1, [1]), (3, [1, 4]), (4, [3])):
+        q, k, v = _randn((B, H, d), act, 1), _randn((sum(nk), G, d), act, 2), _randn((sum(nk), G, d), act, 3)
+        for b, m in enumerate(nk):
+            for x, j in enumerate(back):
+                if j < m:
+                    v[at[b] + m - 1 - j, x % G, 5 + x] = (inf, -inf, float("nan"))[b % 3]
+        out = _prompt(lib, q, k, v, [1] * B, nk, act, d ** -0.5, window, sink)
+        for b, m in enumerate(nk):
+            s = slice(at[b], at[b] + m)
+            want, mag, zmag = gqa.attend(f64(q[b:b + 1]), f64(k[s]), f64(v[s]), [m - 1], d ** -0.5, window, f64(sink))
+            _same(out[b:b + 1], want, mag, zmag, act, f"{m} keys, window {window}")
+
+
+@pytest.mark.parametrize("where", ["first key", "every 97th key", "last key", "every key"])
+@pytest.mark.parametrize("window", [0, 1000])
+def test_prompt_values_that_are_not_finite_take_a_bounded_time(lib, where, window):
+    """A long prompt with NaN among its values: right at every row, and within
+    some 40 times the time without (a warp computes 32 rows again by 16 blocks of
+    16 x 16 for a tile of 128 keys, each a few thousand clocks, as a tile takes
+    otherwise; row by row and key by key it would be 800 times)."""
+    n, H, G, d = 6000, 8, 1, 128
+    q, k, v = _randn((n, H, d), "bf16", 1).cuda(), _randn((n, G, d), "bf16", 2).cuda(), _randn((n, G, d), "bf16", 3).cuda()
+    bad = v.clone()
+    rows = {"first key": [0], "every 97th key": range(0, n, 97), "last key": [n - 1], "every key": range(n)}[where]
+    for j in rows:
+        bad[j, 0, j % d] = float("nan")
+    p = _params(lib, B=1, n_heads=H, n_kv_heads=G, d=d, window=window, softmax_scale=d ** -0.5)
+    cu = _i32([0, n])
+    us = {}
+    for name, x in (("clean", v), ("odd", bad)):
+        out, times = torch.empty_like(q), []
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            lib.gqa_prompt_attn(p, q, k, x, cu, cu, out)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b) * 1e3)
+        us[name] = min(times[1:])
+    t = np.unique(np.concatenate([np.arange(0, 200), np.arange(n - 140, n), np.arange(1000, 1010), np.arange(0, n, 331)]))
+    want, mag, zmag = gqa.attend(f64(q[t.tolist()]), f64(k), f64(bad), t, d ** -0.5, window)
+    _same(out[t.tolist()], want, mag, zmag, "bf16", where)
+    assert us["odd"] < 40 * us["clean"] + 200, us
+
+
 # ---- weights and magnitudes far apart ------------------------------------------
 
 def _sink_like(n, d, act, nats, at, seed):
