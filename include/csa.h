@@ -497,11 +497,13 @@ csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
  * CSA_DEV_ERR_INDEX.  What masked slots hold (infinities and NaN included)
  * does not matter; logits of seen keys must be finite in fp32 (one that is
  * NaN or +infinity makes its query's output NaN).  The scale of
- * an FP8 value counts as no less than 2^-90 and no more than 2^90.  How a
- * sequence's keys are split depends on its own length, T and the window
- * alone, and partial results are joined in a fixed order: a query's output
- * is bit-identical run to run and whatever batch it is in.  Each exp(z_j) is
- * rounded before it weighs its value: to BF16 (2^-8 of itself) for a BF16
+ * an FP8 value counts as no less than 2^-90 and no more than 2^90, and those
+ * that a query sees must lie within a factor of 2^90: beside a larger one, a
+ * key whose value's scale is smaller than that may be missing in the
+ * denominator.  How a sequence's keys are split depends on its own length,
+ * T and the window alone, and partial results are joined in a fixed order: a
+ * query's output is bit-identical run to run and whatever batch it is in.
+ * Each exp(z_j) is rounded before it weighs its value: to BF16 (2^-8 of itself) for a BF16
  * cache, else to FP16 (2^-11 of itself, or 2^-36 of the query's largest where
  * that is more; for an FP8 cache this is about exp(z_j) times the value's
  * scale).  The sums are fp32. */

@@ -333,3 +333,21 @@ def test_equal_logits_of_any_size(lib, act, size):
     _same(_prompt(lib, q, k, v, [n], [n], act, 1.0), want, mag, 0.0, act, "prompt")
     c = Paged([k], [v], 16, "act", act)
     _same(_decode(lib, q[-3:], c.handle(), c.table, [n], 3, act, "act", H, 16, 1.0), want[-3:], mag[-3:], 0.0, act, "decode")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("far", [0, 20, 45])
+def test_decode_fp8_scales_far_apart(lib, d, far):
+    """Value rows up to 2^90 apart in size: small ones still count in the
+    denominator."""
+    n, H, G, page = 400, 4, 2, 16
+    ks, vs = [_randn((n, G, d), "bf16", 1)], [_randn((n, G, d), "bf16", 2)]
+    c = Paged(ks, vs, page, "fp8", "bf16")
+    big = torch.rand(c.v_scale.shape, generator=torch.Generator().manual_seed(4)).cuda() < 0.3
+    c.v_scale.mul_(torch.where(big, 2.0 ** (far + 2), 2.0 ** (2 - far)))
+    q = _randn((3, H, d), "bf16", 3)
+    sink = torch.tensor([0.0, 2.0, -3.0, 1.0])
+    for s in (None, sink):
+        out = _decode(lib, q, c.handle(), c.table, [n], 3, "bf16", "fp8", G, page, d ** -0.5, sink=s)
+        want, mag, zmag = gqa.attend(f64(q), *c.rows(0, n), np.arange(n - 3, n), d ** -0.5, 0, None if s is None else f64(s))
+        _same(out, want, mag, zmag, "bf16")
