@@ -497,7 +497,8 @@ csa_status gqa_cache_append(const gqa_params* params, gqa_rows q, gqa_rows k,
  * CSA_DEV_ERR_INDEX.  What masked slots hold (infinities and NaN included)
  * does not matter; logits of seen keys must be finite in fp32 (one that is
  * NaN or +infinity makes its query's output NaN).  The scale of
- * an FP8 value counts as no less than 2^-90 and no more than 2^90, and those
+ * an FP8 value counts as no less than 2^-90 and no more than 2^90 (an infinite
+ * one as NaN, which 0 times it is), and those
  * that a query sees must lie within a factor of 2^90: beside a larger one, a
  * key whose value's scale is smaller than that may be missing in the
  * denominator.  How a sequence's keys are split depends on its own length,

@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
           for (int e = 0; e < 2; ++e) {
             ks[e] = sc[8 * e];
             const float x = sc[kTile + 8 * e];
-            lv[e] = x != x ? x : fminf(fmaxf(lg2(x), kMinLogScale), kMaxLogScale);
+            lv[e] = x < INFINITY ? fminf(fmaxf(lg2(x), kMinLogScale), kMaxLogScale) : NAN;
             rv[e] = ex2(-lv[e]);
           }
         }

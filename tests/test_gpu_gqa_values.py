@@ -262,6 +262,29 @@ def test_prompt_values_that_are_not_finite_take_a_bounded_time(lib, where, windo
     assert us["odd"] < 40 * us["clean"] + 200, us
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_fp8_row_with_an_infinity(lib, d):
+    """A value row that holds an infinity has it as its scale: whoever sees
+    the row is NaN, whoever does not is exact."""
+    lens, G, H, T, page = [40, 300], 1, 2, 3, 16
+    ks, vs = ([_randn((n, G, d), "bf16", s + b) for b, n in enumerate(lens)] for s in (1, 50))
+    c = Paged(ks, vs, page, "fp8", "bf16")
+    q = _randn((2 * T, H, d), "bf16", 3)
+    rows = [c.rows(b, n) for b, n in enumerate(lens)]
+    for b, j in ((0, 38), (1, 200)):
+        at = c.table[b, j // page].long(), 0, j % page
+        codes = torch.zeros(d, device="cuda")
+        codes[3] = float("nan")
+        c.v[at] = codes.to(torch.float8_e4m3fn)
+        c.v_scale[at] = float("inf")
+    out = _decode(lib, q, c.handle(), c.table, lens, T, "bf16", "fp8", G, page, d ** -0.5)
+    for b, (n, j) in enumerate(zip(lens, (38, 200))):
+        t = np.arange(n - T, n)
+        want, mag, zmag = gqa.attend(f64(q[b * T:(b + 1) * T]), *rows[b], t, d ** -0.5)
+        want[t >= j] = np.nan
+        _same(out[b * T:(b + 1) * T], want, mag, zmag, "bf16", f"length {n}")
+
+
 # ---- weights and magnitudes far apart ------------------------------------------
 
 def _sink_like(n, d, act, nats, at, seed):
