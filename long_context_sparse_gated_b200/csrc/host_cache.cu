@@ -13,7 +13,9 @@
 #include <cuda_runtime.h>
 
 #include <cstring>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "kernels.h"
 
@@ -60,7 +62,7 @@ const DriverFns& driver() {
 struct DeviceFacts {
   unsigned long long ctx = 0;  // context the facts below belong to
   int sms = 0;
-  static constexpr int kMaxKernels = 32;
+  static constexpr int kMaxKernels = 128;  // more than the library has
   const void* kernels[kMaxKernels] = {};
   size_t smem[kMaxKernels] = {};
   int n_kernels = 0;
@@ -97,9 +99,25 @@ struct MapEntry {
   bool used;
 };
 
-constexpr int kMapSlots = 16;
-thread_local MapEntry t_maps[kMapSlots];
-thread_local int t_next = 0;
+// Sets of kWays entries, found by a hash of the key: a step that goes through the
+// layers of a model meets its descriptors again as long as they are about a thousand
+// (a layer's call uses two to four), and calls of one kind do not push out another's.
+constexpr int kSets = 256, kWays = 4;
+struct MapSet {
+  MapEntry way[kWays];
+  int next;  // replaced next
+};
+thread_local std::unique_ptr<MapSet[]> t_maps;
+
+MapSet* set_of(const MapKey& key) {
+  static_assert(sizeof(MapKey) % 8 == 0, "hashed by words");
+  if (!t_maps) t_maps.reset(new (std::nothrow) MapSet[kSets]());
+  if (!t_maps) return nullptr;  // no memory: nothing is kept
+  uint64_t words[sizeof(MapKey) / 8], h = 0;
+  std::memcpy(words, &key, sizeof(key));
+  for (uint64_t w : words) h = (h ^ w) * 0x9E3779B97F4A7C15ull, h ^= h >> 29;
+  return &t_maps[(h >> 32) % kSets];
+}
 
 }  // namespace
 
@@ -160,19 +178,23 @@ bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const
     key.box[i] = box[i];
     if (i + 1 < rank) key.strides[i] = strides_bytes[i];
   }
-  for (int i = 0; i < kMapSlots; ++i)
-    if (t_maps[i].used && std::memcmp(&t_maps[i].key, &key, sizeof(key)) == 0) {
-      *map = t_maps[i].map;
+  MapSet* set = set_of(key);
+  for (int i = 0; set && i < kWays; ++i) {
+    const MapEntry& e = set->way[i];
+    if (e.used && std::memcmp(&e.key, &key, sizeof(key)) == 0) {
+      *map = e.map;
       return true;
     }
+  }
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = d.encode(map, dt, (cuuint32_t)rank, const_cast<void*>(base), (const cuuint64_t*)dims,
                               (const cuuint64_t*)strides_bytes, (const cuuint32_t*)box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
-  MapEntry& e = t_maps[t_next];
-  t_next = (t_next + 1) % kMapSlots;
+  if (!set) return true;
+  MapEntry& e = set->way[set->next];
+  set->next = (set->next + 1) % kWays;
   e.key = key;
   e.map = *map;
   e.used = true;
