@@ -390,7 +390,7 @@ def _rows(x, dtype, device, n, heads, d):
     if x.dtype is not dtype or x.get_device() != device or sd != 1 or x.shape != (n, heads, d):
         _refuse(x, dtype, device, (n, heads, d))
     # the stride of a single row or head is never used
-    return GqaRows(x.data_ptr(), sn if n > 1 else max(sn, d), sh if heads > 1 else max(sh, d))
+    return GqaRows(x.data_ptr(), sn if n > 1 else d, sh if heads > 1 else d)
 
 
 def _gqa_call(params):

@@ -65,3 +65,26 @@ def decode(n_max, window):
 print([decode(n, w) for n in ((1 << 30) - 1, 1 << 30, (1 << 30) + (1 << 20), (1 << 31) - 257) for w in (0, 1 << 30)])
 """
     assert _run(code) == [(-4, True)] * 2 + [(-2, False)] * 6
+
+
+def test_strides_of_a_single_row_or_head_do_not_count():
+    """A view of one row or one head may have any stride there (rows of a
+    tensor whose width is no multiple of 8, a broadcast dim)."""
+    import torch
+
+    import long_context_sparse_gated_b200 as lib
+
+    class OnDevice(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    def rows(x, n, heads):
+        r = lib._rows(x.as_subclass(OnDevice), torch.bfloat16, 0, n, heads, 64)
+        return r.row_stride, r.head_stride
+
+    x = torch.zeros(5, 4 * 64 + 3, dtype=torch.bfloat16)
+    assert rows(x[:1, :256].view(1, 4, 64), 1, 4) == (64, 64)
+    y = torch.zeros(6, 3, 64, dtype=torch.bfloat16)
+    assert rows(y.as_strided((6, 1, 64), (192, 1, 1)), 6, 1) == (192, 64)
+    assert rows(y.as_strided((1, 3, 64), (0, 64, 1)), 1, 3) == (64, 64)
+    assert rows(y, 6, 3) == (192, 64) and rows(y.transpose(0, 1), 3, 6) == (64, 192)
