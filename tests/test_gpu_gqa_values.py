@@ -230,6 +230,23 @@ def test_prompt_one_query_behind_a_value_that_is_not_finite(lib, act, d):
             _same(out[b:b + 1], want, mag, zmag, act, f"{m} keys, window {window}")
 
 
+@pytest.mark.parametrize("T,H,G", [(1, 4, 2), (3, 4, 2), (5, 8, 2)])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_decode_infinities_in_values(lib, act, T, H, G):
+    d, page, inf = 64, 16, float("inf")
+    lens = [50, 700, 67]
+    ks, vs = ([_randn((n, G, d), act, s + b) for b, n in enumerate(lens)] for s in (1, 50))
+    vs[0][-1, 0, 5], vs[0][-2, 0, 6], vs[1][-1, 1, 7], vs[1][3, 0, 8] = inf, -inf, -inf, inf
+    vs[2][-1, 0, 9], vs[2][20, 0, 9], vs[2][-1, 1, 9] = inf, -inf, inf
+    c = Paged(ks, vs, page, "act", act)
+    q = _randn((len(lens) * T, H, d), act, 3)
+    for window in (0, 40):
+        out = _decode(lib, q, c.handle(), c.table, lens, T, act, "act", G, page, d ** -0.5, window)
+        for b, n in enumerate(lens):
+            want, mag, zmag = gqa.attend(f64(q[b * T:(b + 1) * T]), *c.rows(b, n), np.arange(n - T, n), d ** -0.5, window)
+            _same(out[b * T:(b + 1) * T], want, mag, zmag, act, f"length {n}, window {window}")
+
+
 @pytest.mark.parametrize("where", ["first key", "every 97th key", "last key", "every key"])
 @pytest.mark.parametrize("window", [0, 1000])
 def test_prompt_values_that_are_not_finite_take_a_bounded_time(lib, where, window):
@@ -374,3 +391,60 @@ def test_decode_fp8_scales_far_apart(lib, d, far):
         out = _decode(lib, q, c.handle(), c.table, [n], 3, "bf16", "fp8", G, page, d ** -0.5, sink=s)
         want, mag, zmag = gqa.attend(f64(q), *c.rows(0, n), np.arange(n - 3, n), d ** -0.5, 0, None if s is None else f64(s))
         _same(out, want, mag, zmag, "bf16")
+
+
+# ---- batches and host threads --------------------------------------------------
+
+def test_prompt_bits_do_not_depend_on_the_batch(lib):
+    lens, H, G, d = [700, 40, 256, 1, 129], 6, 2, 128
+    n = sum(lens)
+    q, k, v = _randn((n, H, d), "bf16", 1), _randn((n, G, d), "bf16", 2), _randn((n, G, d), "bf16", 3)
+    whole, at = _prompt(lib, q, k, v, lens, lens, "bf16", d ** -0.5), 0
+    for m in lens:
+        s = slice(at, at + m)
+        assert torch.equal(_prompt(lib, q[s], k[s], v[s], [m], [m], "bf16", d ** -0.5), whole[s])
+        at += m
+
+
+def test_two_host_threads(lib):
+    """Two threads with a stream, a cache and a workspace each, of different
+    forms, give what they give alone."""
+    def layer(i):
+        act, kv, d, page, H, G, n = (("bf16", "act", 128, 32, 8, 2, 900), ("f16", "fp8", 64, 16, 6, 1, 700))[i]
+        c = Paged([_randn((n, G, d), act, 1 + i)], [_randn((n, G, d), act, 3 + i)], page, kv, act, extra_cols=3)
+        c.table[0, -(-n // page):] = c.k.shape[0] - 1
+        p = _params(lib, act, kv, B=1, n_heads=H, n_kv_heads=G, d=d, r=d, page=page, softmax_scale=d ** -0.5, rope_theta=(1e4, 5e5)[i])
+        q, new = _randn((3, H, d), act, 5 + i).cuda(), _randn((3, G, d), act, 7 + i).cuda()
+        ws = torch.empty(max(16, lib.gqa_decode_attn_workspace_bytes(p, 3, n + 3)), dtype=torch.uint8, device="cuda")
+        cu, pos0, lens = _i32([0, 3]), _i32([n]), _i32([n + 3])
+
+        def step():
+            qo, ko, out, po = torch.empty_like(q), torch.empty_like(new), torch.empty_like(q), torch.empty_like(q)
+            lib.gqa_cache_append(p, q, new, new, cu, pos0, c.handle(), c.table, q_out=qo, k_out=ko)
+            lib.gqa_decode_attn(p, qo, c.handle(), c.table, lens, 3, n + 3, out, ws)
+            lib.gqa_prompt_attn(p, qo, ko, new, cu, cu, po)
+            return qo, ko, out, po
+        return step
+
+    layers = [layer(0), layer(1)]
+    alone = [f() for f in layers]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(200):
+                    got = layers[i]()
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, alone[i])):
+                    wrong.append(f"thread {i}: other bits")
+        except Exception as e:  # noqa: BLE001
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
