@@ -1,5 +1,5 @@
-// Shared by the grouped-query attention kernels (gqa_*.cu): 16-bit
-// activation types, rotation of 8-element pieces of a row, mask bounds.
+// Shared by the grouped-query attention kernels (gqa_*.cu): 16-bit activation
+// types, a few inline instructions, the 16-bit mma.sync.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -9,9 +9,8 @@
 namespace csa {
 namespace gqa {
 
-// 2^x and 1/x to about an fp32 step, inline.  (The precise division is a
-// subroutine: the first call in a launch fetches it, which took the prompt
-// kernel's softmax 5000 clocks.)
+// 2^x and 1/x to about an fp32 step, inline.  (With the precise division in their
+// place the prompt kernel's softmax lost 5000 clocks in every launch.)
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

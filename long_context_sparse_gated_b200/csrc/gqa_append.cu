@@ -8,7 +8,8 @@
 // thread are on their way before one warp per token looks up its sequence, position
 // and page and fills the token's cosines and sines (one pair per rotated pair
 // of dims, shared by all heads) in shared memory.  22730 tokens of 32 + 16 heads
-// of 128: 102 us, 92% of the copy rate; into an FP8 cache 101 us, 86%.
+// of 128: 109 us through the binding, 86% of the copy rate; into an FP8 cache 105 us,
+// 83%.
 //
 // Angles.  pos * theta^(-2j/r) in turns: the frequencies / 2 pi come from the
 // host in fp64, the product is reduced to [-1/2, 1/2] turns in fp64 and only
@@ -17,7 +18,7 @@
 // FP8.  The lanes that hold a row agree on its largest magnitude.  The scale
 // is amax * (1/448) and codes are those of value * (1 / scale): both differ from
 // the quotients by an fp32 rounding or two (a code only where the quotient is
-// that near a border), and there is no division subroutine to fetch.
+// that near a border).  Only rows whose 1 / scale is beyond fp32 are divided.
 #include <cmath>
 #include <cstring>
 
@@ -239,8 +240,8 @@ cudaError_t launch_gqa_append(const gqa_params& p, const gqa_rows& q, const gqa_
                               int32_t* err, cudaStream_t st) {
   // tokens per CTA: as many as fill the threads' first batch of loads, but no
   // fewer CTAs than SMs.  Three pieces a thread where that leaves fewer threads
-  // idle than two do (us with two / three: 32 + 16 heads of 128 106 / 103, FP8 122 /
-  // 101, of 64 60 / 56; 64 + 16 heads, as many idle either way, 157 / 162).
+  // idle than two do (us with two / three, in short runs: 32 + 16 heads of 128 106 /
+  // 103, FP8 122 / 101, of 64 60 / 56; 64 + 16 heads, as many idle either way, 157 / 162).
   const int nq = q.ptr ? p.n_heads : 0, per_token = nq + 2 * p.n_kv_heads, pieces = per_token * p.d / 16;
   const int64_t most = n_tokens / sm_count();
   auto tokens_of = [&](int batch) {

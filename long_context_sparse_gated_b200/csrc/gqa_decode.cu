@@ -28,18 +28,18 @@
 //   rows     8, 16 or 32 an item, so that several tokens and large groups do not
 //            read the cache twice. With 32 the sums leave no registers for the
 //            queries, whose fragments and positions wait in shared memory.  40
-//            sequences of up to 1152 keys, 4 tokens, 40 / 8 heads: 44 us, in items
-//            of 16 rows 67; 8 of up to 20000, 64 / 8 heads: 112 and 125, FP8 122 and
-//            157.  (Two warps a scheduler then wait for their own instructions, some
-//            4000 clocks a tile: 112 us are 62% of the copy rate.)
+//            sequences of up to 1152 keys, 4 tokens, 40 / 8 heads: 43 us, in items
+//            of 16 rows 48; 8 of up to 20000, 64 / 8 heads: 110 and 122, FP8 119 and
+//            151.  (Two warps a scheduler then wait for their own instructions, some
+//            4000 clocks a tile: 110 us are 62% of the copy rate.)
 //
 // 16-bit cache.  m16n8k16; K by ldmatrix, V by ldmatrix.trans, P^T rounded to
 // 16 bits and transposed in registers by movmatrix.
 //
 // FP8 cache.  E4M3 codes become FP16 in registers by the packed conversion
-// instruction (moving the bits by hand takes 163 us instead of 129 for 24
-// sequences of up to 32K keys; m16n8k32 on 8-bit operands is no way around it:
-// here it compiles to conversions and m16n8k16).  The dims of a 16-byte piece
+// instruction (moving the bits by hand took 163 us instead of 129 for 24
+// sequences of up to 32K keys, m16n8k32 on the codes and weights split into E5M2 pieces
+// 263 to 358; now 134).  The dims of a 16-byte piece
 // are dealt to MMA steps in an order that Q's fragments share, so no shuffles
 // are needed.  A query row is brought into FP16 by a power of two of its own
 // (largest magnitude in [2^14, 2^15); what is 2^29 below that loses bits that do
@@ -95,9 +95,10 @@ constexpr float kMinLogScale = -90.f, kMaxLogScale = 90.f;
 // Blocks per split for a sequence of n blocks: 8, 16 or 32 blocks, so that
 // there are about 12 splits (256 to 1024 keys), and 64 for more than 64K keys.
 // Measured (32 mixed up to 16K / 4 of 128K / 24 FP8 up to 32K / 16 x 4 drafted
-// tokens, us): this 151 / 326 / 128 / 15; 4 to 16 blocks and 32 splits 160 / 360 /
-// 140 / 18; never 64 blocks 151 / 339 / 128 / 15; 4 blocks at least 155 / 326 / 128 /
-// 18; 16 at least 147 / 326 / 127 / 15, but 16.4 instead of 14.1 for 777 keys alone.
+// tokens / 777 keys alone, us, one call from cold caches): this 172 / 342 / 143 / 20 /
+// 14; 4 to 16 blocks and 32 splits 180 / 371 / 152 / 25 / 14; never 64 blocks 172 / 362 /
+// 141 / 20 / 14; 4 blocks at least 174 / 342 / 143 / 25 / 14; 16 at least 169 / 342 / 141 /
+// 20 / 16.
 constexpr int kMinSplit = 8, kMidSplit = 32, kMaxSplit = 64, kSplits = 12, kLong = 2048;
 __host__ __device__ inline int split_blocks(int n) {
   if (n > kLong) return kMaxSplit;

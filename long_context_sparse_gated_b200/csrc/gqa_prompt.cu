@@ -21,15 +21,15 @@
 //             TMEM, in two halves, so that the product with the first 64 keys
 //             begins while the second half is computed.  The maximum moves
 //             only when a row exceeds it by 2^8 (FP16: 2^6), so O is hardly ever
-//             rescaled;
-//             at the end the same threads normalise O and write it out
-//             through shared memory.
+//             rescaled; at the end the same threads normalise O and write it
+//             out through shared memory.
 //
 // Exponentials.  A tile pair has 32768 of them: 2048 clocks of the 16-lane
 // special-function pipe, as many as its four products take.  So kPoly of
-// every 8 pairs of logits (3 for BF16, 2 for FP16; 16K tokens take 417 us with
-// 3, 425 with 2, 446 with 1, 474 with none) go through the FMA pipe instead: 2^x =
-// 2^n 2^f with n the nearest integer (by adding 1.5 * 2^23) and a polynomial in f,
+// every 8 pairs of logits (3 for BF16, 2 for FP16; 16K tokens, one call from cold
+// caches, take 452 us with 4, 422 with 3, 426 with 2, 442 with 1, 430 with none; FP16
+// 442 with 3, 440 with 2, 455 with 1, 443 with none) go through the FMA pipe instead:
+// 2^x = 2^n 2^f with n the nearest integer (by adding 1.5 * 2^23) and a polynomial in f,
 // minimax for the relative error on [-1/2, 1/2]: degree 3, 7.5e-5, before P is
 // rounded to BF16 (2^-8), degree 4, 2.6e-6, before FP16 (2^-11).  n is added to
 // the exponent field; weights below 2^-126 (2^-98 of the row's largest and less)
@@ -67,8 +67,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Weights are 2^(z - m + kTop) with m a running maximum, raised when a logit
 // exceeds it by kLazy (base-2 units).  FP16 holds weights from 2^-14 (with fewer bits
 // from 2^-24) to 2^16, so the largest are put near its top, the nearer the closer the
-// maximum is followed (16K tokens, FP16, 8/1 heads of 128: by 2^8 430 us, 2^6 432, 2^4
-// 451).  BF16 weights stay below 2^-20, so that sums of the type's largest values over
+// maximum is followed (16K tokens, FP16, 8/1 heads of 128: by 2^8 438 us, 2^6 440, 2^4
+// 461).  BF16 weights stay below 2^-20, so that sums of the type's largest values over
 // 2^20 keys are finite.
 template <bool kBf16>
 struct Weights {
@@ -133,9 +133,8 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&u)[
       : "memory");
 }
 // Whether this lane is the one of its warp that issues MMAs.  The rest of the
-// warp runs along, so that descriptors stay in uniform registers: issued from
-// a branch on the lane index, an MMA took some 118 clocks to issue, twice what
-// it takes to run.
+// warp runs along: issued from a branch on the lane index, an MMA took some 118
+// clocks to issue, twice what it takes to run.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -380,7 +379,8 @@ __device__ __noinline__ void blocks_again(const PromptArgs& a, unsigned rows, in
 
 // A lone such row near a sequence's beginning is computed by itself, a lane with kD/32
 // dims of it.  (16 keys take it as long as blocks_again, and with this path in it the
-// kernel around takes 416 us for 16K tokens instead of 440.)
+// kernel around takes 416 us for 16K tokens instead of 440: what registers the code
+// out of line takes changes those of the softmax.)
 template <bool kBf16, int kD>
 __device__ __noinline__ void rows_again(const PromptArgs& a, unsigned odd, int key0, int key1, int row, int t, int head, int kvh,
                                         int k0, int lane) {
