@@ -81,11 +81,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Weights are 2^(z - m) with m = a running maximum - kTop, raised when a logit
 // exceeds the maximum by kLazy (base-2 units).  FP16 holds weights from 2^-14
 // (with fewer bits from 2^-24) to 2^16, so the largest are put near its top.  BF16
-// weights stay below 2^-20, so that sums of the type's largest values over 2^20 keys
-// are finite.
+// weights begin at 2^-14: sums of the type's largest values stay finite while the
+// weights add up to less than 2^14 of the largest, and products with its smallest
+// are still well above fp32's last bit.
 template <bool kBf16>
 struct Weights {
-  static constexpr float kTop = kBf16 ? -28.f : 11.f, kLazy = kBf16 ? 8.f : 4.f;
+  static constexpr float kTop = kBf16 ? -14.f : 11.f, kLazy = kBf16 ? 8.f : 4.f;
 };
 constexpr float kNone = -3.0e38f;  // a running maximum before the first key
 struct Edge { static constexpr bool value = true; };

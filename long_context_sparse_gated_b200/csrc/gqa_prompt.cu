@@ -32,7 +32,7 @@
 // 2^x = 2^n 2^f with n the nearest integer (by adding 1.5 * 2^23) and a polynomial in f,
 // minimax for the relative error on [-1/2, 1/2]: degree 3, 7.5e-5, before P is
 // rounded to BF16 (2^-8), degree 4, 2.6e-6, before FP16 (2^-11).  n is added to
-// the exponent field; weights below 2^-126 (2^-98 of the row's largest and less)
+// the exponent field; weights below 2^-126 (2^-112 of the row's largest and less)
 // come out as about that.  Packed fp32 pairs (f32x2) throughout.
 //
 // Masks.  In tiles that some row does not see as a whole logits are selected,
@@ -68,11 +68,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 // exceeds it by kLazy (base-2 units).  FP16 holds weights from 2^-14 (with fewer bits
 // from 2^-24) to 2^16, so the largest are put near its top, the nearer the closer the
 // maximum is followed (16K tokens, FP16, 8/1 heads of 128: by 2^8 438 us, 2^6 440, 2^4
-// 461).  BF16 weights stay below 2^-20, so that sums of the type's largest values over
-// 2^20 keys are finite.
+// 461).  BF16 weights begin at 2^-14: sums of the type's largest values stay finite
+// while the weights add up to less than 2^14 of the largest, and products with its
+// smallest are still well above fp32's last bit.
 template <bool kBf16>
 struct Weights {
-  static constexpr float kTop = kBf16 ? -28.f : 9.5f, kLazy = kBf16 ? 8.f : 6.f;
+  static constexpr float kTop = kBf16 ? -14.f : 9.5f, kLazy = kBf16 ? 8.f : 6.f;
 };
 
 struct PromptArgs {
@@ -228,8 +229,8 @@ __device__ __forceinline__ bool odd8(const uint4& v) {
   return ((top(v.x) | top(v.y) | top(v.z) | top(v.w)) & 0x80008000u) != 0;
 }
 
-// Rows of a unit that came out as something not finite (32 rows from packed query row
-// `row` and position `t` on, `odd` says which), looked at again by their warp.  They
+// Rows of a unit that came out as something not finite (those of `rows` of the 32 from
+// packed query row row0, at position t0, on), looked at again by their warp.  They
 // stay as they are unless a value that is not finite lies in one of the unit's tiles
 // (keys [key0, key1)) where not all of them see it; it has then reached rows that do
 // not see it as 0 * NaN.  Such rows are computed again, 16 rows by 16 keys at a time
@@ -378,9 +379,9 @@ __device__ __noinline__ void blocks_again(const PromptArgs& a, unsigned rows, in
 }
 
 // A lone such row near a sequence's beginning is computed by itself, a lane with kD/32
-// dims of it.  (16 keys take it as long as blocks_again, and with this path in it the
-// kernel around takes 416 us for 16K tokens instead of 440: what registers the code
-// out of line takes changes those of the softmax.)
+// dims of it.  (32000 such rows of 8 keys take 0.39 ms, by blocks 0.47, of 44 keys 0.96
+// and 1.04; and with this path the kernel around takes 416 us for 16K tokens, not 440:
+// what registers the code out of line takes changes those of the softmax.)
 template <bool kBf16, int kD>
 __device__ __noinline__ void rows_again(const PromptArgs& a, unsigned odd, int key0, int key1, int row, int t, int head, int kvh,
                                         int k0, int lane) {

@@ -361,6 +361,23 @@ def test_values_at_the_end_of_the_type(lib, act, d):
         _same(out, want[-T:], mag[-T:], zmag, act, "decode")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** -118, 2.0 ** -100, 2.0 ** 100])
+def test_values_far_from_one(lib, d, size):
+    """BF16 values of 2^-118 and 2^100 on average weigh as those of 1 do.  (fp32
+    sums lose 2^-149 a product at most; with weights of 2^-18 on average that is
+    2^-131 of the result, 2^-13 of values of 2^-118.)"""
+    n, H, G, page = 700, 4, 2, 32
+    q, k = _randn((n, H, d), "bf16", 1), _randn((n, G, d), "bf16", 2)
+    v = (_randn((n, G, d), "bf16", 3).float() * size).bfloat16()
+    want, mag, zmag = gqa.attend(f64(q), f64(k), f64(v), np.arange(n), d ** -0.5)
+    _same(_prompt(lib, q, k, v, [n], [n], "bf16", d ** -0.5), want, mag, zmag, "bf16", "prompt")
+    c = Paged([k], [v], page, "act", "bf16")
+    for T in (1, 9):
+        out = _decode(lib, q[-T:], c.handle(), c.table, [n], T, "bf16", "act", G, page, d ** -0.5)
+        _same(out, want[-T:], mag[-T:], zmag, "bf16", "decode")
+
+
 @pytest.mark.parametrize("act,size", [("f16", 6e4), ("bf16", 3e3), ("bf16", 1e9), ("bf16", 5e17)])
 def test_equal_logits_of_any_size(lib, act, size):
     """Logits of up to 10^37, all equal: the average of the values."""
