@@ -606,7 +606,9 @@ __global__ void __launch_bounds__(32 * Layout<kFp8, kD, kNq>::kWarps, 1)
               float v = fmaxf(z[nt][e], z[nt][e + 2]);
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
               v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16)) - kTop;
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+              // (where fp32's step is larger than kTop, to the maximum itself)
+              v = kTop < 0.f ? __fadd_rd(v, -kTop) : __fadd_ru(v, -kTop);
               alpha[e] = 1.f;
               if (v > m[nt][e]) {
                 alpha[e] = ex2(m[nt][e] - v);  // 0 from kNone

@@ -392,6 +392,23 @@ def test_equal_logits_of_any_size(lib, act, size):
     _same(_decode(lib, q[-3:], c.handle(), c.table, [n], 3, act, "act", H, 16, 1.0), want[-3:], mag[-3:], 0.0, act, "decode")
 
 
+@pytest.mark.parametrize("act,kv", [("f16", "act"), ("bf16", "act"), ("bf16", "fp8"), ("f16", "fp8")])
+def test_decode_equal_logits_around_fp32s_last_bit(lib, act, kv):
+    """Logits of 10^6 to 10^10, where fp32's step goes from a fraction to more
+    than all that a weight's range holds: still the average.  (With an FP8 cache
+    the value's log-scale shares the logit's rounding, as any error of a logit.)"""
+    n, H, d = 150, 2, 128
+    v = [_randn((n, H, d), act, 3)]
+    for size in (128.0, 256.0, 512.0, 736.0, 1040.0, 1472.0, 2080.0, 4160.0, 8320.0):
+        q, k = torch.full((3, H, d), size).to(ACT[act]), torch.full((n, H, d), size).to(ACT[act])
+        q[:, 1] *= -1
+        c = Paged([k], v, 16, kv, act)
+        x = c.rows(0, n)[1]
+        want, mag = (np.stack([y[:m].mean(0) for m in (n - 2, n - 1, n)]) for y in (x, np.abs(x)))
+        _same(_decode(lib, q, c.handle(), c.table, [n], 3, act, kv, H, 16, 1.0), want, mag,
+              0.0 if kv == "act" else 128 * size * size, act, f"{kv} {size}")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("far", [0, 20, 45])
 def test_decode_fp8_scales_far_apart(lib, d, far):
